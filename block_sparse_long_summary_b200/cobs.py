@@ -36,7 +36,8 @@ EXPORTED = [
     "cobs_build_summaries", "cobs_select", "cobs_sparse_attn_decode", "cobs_sparse_attn_prefill",
     "cobs_sparse_attn_decode_noalloc", "cobs_workspace_bytes", "cobs_summaries_elems", "cobs_status_string", "cobs_last_error",
     "cobs_device_error", "cobs_launch_count", "cobs_version", "cobs_block_log_mass", "cobs_decode_step",
-    "cobs_decode_step_fused", "cobs_query_basis",
+    "cobs_decode_step_fused", "cobs_query_basis", "cobs_paged_tables", "cobs_paged_append", "cobs_paged_attn",
+    "cobs_paged_workspace_bytes",
 ]
 
 
@@ -46,6 +47,12 @@ class cobs_params(ctypes.Structure):
                 ("cmp_stride", ctypes.c_int32), ("topk", ctypes.c_int32), ("window", ctypes.c_int32),
                 ("alpha", ctypes.c_float), ("dtype", ctypes.c_int32), ("variance", ctypes.c_int32),
                 ("rank", ctypes.c_int32), ("sub", ctypes.c_int32), ("basis", ctypes.c_void_p)]
+
+
+class cobs_paged_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("R", "Hq", "Hkv", "d", "page", "n_pages", "max_pages", "n_tokens", "max_new",
+                                              "window", "sinks", "dtype")] + [("q_stride", ctypes.c_int64),
+                                                                              ("kv_stride", ctypes.c_int64)]
 
 
 class CobsError(RuntimeError):
@@ -74,6 +81,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     for f in ("cobs_build_summaries", "cobs_select", "cobs_sparse_attn_decode", "cobs_sparse_attn_prefill",
               "cobs_sparse_attn_decode_noalloc", "cobs_block_log_mass", "cobs_decode_step", "cobs_decode_step_fused"):
         getattr(lib, f).restype = ctypes.c_int
+    PP = ctypes.POINTER(cobs_paged_params)
+    lib.cobs_paged_tables.argtypes = [PP, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.cobs_paged_append.argtypes = [PP, vp, vp, vp, vp, vp, vp]
+    lib.cobs_paged_attn.argtypes = [PP, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    for f in ("cobs_paged_tables", "cobs_paged_append", "cobs_paged_attn"):
+        getattr(lib, f).restype = ctypes.c_int
+    lib.cobs_paged_workspace_bytes.argtypes = [PP]
+    lib.cobs_paged_workspace_bytes.restype = sz
     lib.cobs_workspace_bytes.argtypes = [P, i32]
     lib.cobs_workspace_bytes.restype = sz
     lib.cobs_summaries_elems.argtypes = [P]
@@ -321,3 +336,169 @@ def prefill(p: Params, Q, K, V, Pk, Pv, gates, buf: Buffers, stream=None):
     cobs_build_summaries(p, K, V, Pk, Pv, 0, buf.summaries, buf.Kc, buf.Vc, stream)
     cobs_select(p, Q, buf.summaries, 1, buf.idx, buf.ws_select, stream)
     cobs_sparse_attn_prefill(p, Q, K, V, buf.Kc, buf.Vc, buf.idx, gates, buf.O, buf.ws_attn, stream)
+
+
+# -------------------------------------------------------------- paged cache (requests of different lengths)
+
+@dataclasses.dataclass(frozen=True)
+class PagedParams:
+    """Problem statement of the paged-cache calls (see include/cobs.h). Frozen, so that the C struct
+    is made once; dataclasses.replace() makes a changed copy."""
+    R: int
+    Hq: int
+    Hkv: int
+    d: int
+    page: int
+    n_pages: int
+    max_pages: int
+    n_tokens: int
+    max_new: int
+    window: int = 0
+    sinks: int = 0
+    dtype: str = "bf16"
+    _structs: dict = dataclasses.field(default_factory=dict, init=False, compare=False, repr=False)
+
+    def c(self, q_stride: int = 0, kv_stride: int = 0) -> cobs_paged_params:
+        cp = self._structs.get((q_stride, kv_stride))
+        if cp is None:
+            if self.dtype not in ("bf16", "f32"):
+                raise ValueError(f"dtype {self.dtype!r} (bf16 or f32)")
+            cp = cobs_paged_params(self.R, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages,
+                                   self.n_tokens, self.max_new, self.window, self.sinks,
+                                   COBS_BF16 if self.dtype == "bf16" else COBS_F32, q_stride, kv_stride)
+            self._structs[q_stride, kv_stride] = cp
+        return cp
+
+    @property
+    def torch_dtype(self):
+        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+
+
+def _arg(t, name: str, dtype, numel: int, dev: int) -> int:
+    """Address of a contiguous tensor of the given type and size on device `dev`."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on CUDA device {dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {numel} elements, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, p: PagedParams, heads: int, dev: int):
+    """Address and token stride of [n_tokens, heads, d] rows (each token's heads contiguous)."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on CUDA device {dev}")
+    if t.dtype is not p.torch_dtype:
+        raise ValueError(f"{name} must be {p.torch_dtype}, not {t.dtype}")
+    if t.shape != (p.n_tokens, heads, p.d):
+        raise ValueError(f"{name} must be [{p.n_tokens}, {heads}, {p.d}], got {tuple(t.shape)}")
+    st = t.stride()
+    if p.n_tokens == 0:
+        return None, 0
+    if st[2] != 1 or (heads > 1 and st[1] != p.d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if p.n_tokens == 1 or st[0] == heads * p.d:
+        return t.data_ptr(), 0
+    if st[0] < heads * p.d:
+        raise ValueError(f"{name}: token rows overlap")
+    return t.data_ptr(), st[0]
+
+
+def _device_of(t) -> int:
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    return t.get_device()
+
+
+def _call(dev: int, stream, fn, *args):
+    """Enqueue on `stream` (default: the current one of the tensors' device), that device current."""
+    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        _check(fn(*args, raw))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, raw))
+
+
+def paged_workspace_bytes(p: PagedParams) -> int:
+    return int(_lib.cobs_paged_workspace_bytes(ctypes.byref(p.c())))
+
+
+def alloc_paged_workspace(p: PagedParams, device="cuda") -> torch.Tensor:
+    """Scratch of cobs_paged_attn (one per call that may run at the same time as another)."""
+    dev = torch.device(device)
+    with torch.cuda.device(dev):
+        n = paged_workspace_bytes(p)
+        if n == 0:
+            raise CobsError(COBS_ERR_INVALID_ARG, _lib.cobs_last_error().decode())
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def cobs_paged_tables(p: PagedParams, cached_len, new_len, free_pages, free_count, block_table, cu_new, kv_len, slot_map,
+                      counts, stream=None):
+    """Block-table entries of the pages that the new tokens open, slot map and running sums, from the lengths."""
+    dev, i32 = _device_of(cached_len), torch.int32
+    _call(dev, stream, _lib.cobs_paged_tables, ctypes.byref(p.c()), _arg(cached_len, "cached_len", i32, p.R, dev),
+          _arg(new_len, "new_len", i32, p.R, dev), _arg(free_pages, "free_pages", i32, free_pages.numel(), dev) or None,
+          free_pages.numel(), _arg(free_count, "free_count", i32, 1, dev),
+          _arg(block_table, "block_table", i32, p.R * p.max_pages, dev), _arg(cu_new, "cu_new", i32, p.R + 1, dev),
+          _arg(kv_len, "kv_len", i32, p.R, dev), _arg(slot_map, "slot_map", i32, p.n_tokens, dev) or None,
+          _arg(counts, "counts", i32, 4, dev))
+
+
+def cobs_paged_append(p: PagedParams, K, V, slot_map, k_cache, v_cache, stream=None):
+    """Copy the new K and V rows to the slots of the caches."""
+    dev = _device_of(k_cache)
+    k, ks = _rows(K, "K", p, p.Hkv, dev)
+    v, vs = _rows(V, "V", p, p.Hkv, dev)
+    if ks != vs:
+        raise ValueError("K and V must have the same token stride")
+    n = p.n_pages * p.Hkv * p.page * p.d
+    _call(dev, stream, _lib.cobs_paged_append, ctypes.byref(p.c(0, ks)), k, v,
+          _arg(slot_map, "slot_map", torch.int32, p.n_tokens, dev) or None, _arg(k_cache, "k_cache", p.torch_dtype, n, dev),
+          _arg(v_cache, "v_cache", p.torch_dtype, n, dev))
+
+
+def cobs_paged_attn(p: PagedParams, Q, k_cache, v_cache, block_table, cu_new, kv_len, O, lse, workspace, stream=None):
+    """Attention of every request's new tokens over its pages (lse: [n_tokens, Hq] float32, or None)."""
+    dev, i32 = _device_of(k_cache), torch.int32
+    q, qs = _rows(Q, "Q", p, p.Hq, dev)
+    n = p.n_pages * p.Hkv * p.page * p.d
+    _call(dev, stream, _lib.cobs_paged_attn, ctypes.byref(p.c(qs)), q, _arg(k_cache, "k_cache", p.torch_dtype, n, dev),
+          _arg(v_cache, "v_cache", p.torch_dtype, n, dev), _arg(block_table, "block_table", i32, p.R * p.max_pages, dev),
+          _arg(cu_new, "cu_new", i32, p.R + 1, dev), _arg(kv_len, "kv_len", i32, p.R, dev),
+          _arg(O, "O", p.torch_dtype, p.n_tokens * p.Hq * p.d, dev) or None,
+          None if lse is None else _arg(lse, "lse", torch.float32, p.n_tokens * p.Hq, dev) or None,
+          _arg(workspace, "workspace", torch.uint8, workspace.numel(), dev), workspace.numel())
+
+
+@dataclasses.dataclass
+class PagedBuffers:
+    """Tables, outputs and workspace of one batch (see alloc_paged)."""
+    block_table: torch.Tensor
+    cu_new: torch.Tensor
+    kv_len: torch.Tensor
+    slot_map: torch.Tensor
+    counts: torch.Tensor
+    O: torch.Tensor
+    ws: torch.Tensor
+
+
+def alloc_paged(p: PagedParams, device="cuda") -> PagedBuffers:
+    """The tables (no pages), output and workspace of one batch."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return PagedBuffers(torch.full((p.R, p.max_pages), -1, **i32), torch.zeros(p.R + 1, **i32), torch.zeros(p.R, **i32),
+                        torch.full((p.n_tokens,), -1, **i32), torch.zeros(4, **i32),
+                        torch.zeros((p.n_tokens, p.Hq, p.d), dtype=p.torch_dtype, device=device),
+                        alloc_paged_workspace(p, device))
+
+
+def paged_step(p: PagedParams, Q, K, V, cached_len, new_len, free_pages, free_count, k_cache, v_cache,
+               buf: PagedBuffers, lse=None, stream=None):
+    """One step of one layer: tables from the lengths, append of the new keys and values, attention.
+    A program of several layers calls cobs_paged_tables once and the other two per layer."""
+    cobs_paged_tables(p, cached_len, new_len, free_pages, free_count, buf.block_table, buf.cu_new, buf.kv_len, buf.slot_map,
+                      buf.counts, stream)
+    cobs_paged_append(p, K, V, buf.slot_map, k_cache, v_cache, stream)
+    cobs_paged_attn(p, Q, k_cache, v_cache, buf.block_table, buf.cu_new, buf.kv_len, buf.O, lse, buf.ws, stream)

@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "dims.h"
+#include "paged.h"
 
 namespace {
 
@@ -110,6 +111,42 @@ cobs_status check_ptr(const void* ptr, const char* name, bool may_be_null = fals
         return fail(COBS_ERR_INVALID_ARG, "%s is NULL", name);
     }
     if (!aligned16(ptr)) return fail(COBS_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+    return COBS_OK;
+}
+
+// int32 arrays of the paged calls (a slice of a larger array will do)
+cobs_status check_ints(const int32_t* ptr, const char* name) {
+    if (ptr == nullptr) return fail(COBS_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(ptr) & 3u) return fail(COBS_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
+    return COBS_OK;
+}
+
+cobs_status validate_paged(const cobs_paged_params* p) {
+    if (p == nullptr) return fail(COBS_ERR_INVALID_ARG, "params is NULL");
+    if (p->R < 1 || p->Hq < 1 || p->Hkv < 1 || p->n_pages < 1 || p->max_pages < 1 || p->max_new < 1)
+        return fail(COBS_ERR_INVALID_ARG, "R, Hq, Hkv, n_pages, max_pages and max_new must be >= 1 (got %d, %d, %d, %d, %d, %d)",
+                    p->R, p->Hq, p->Hkv, p->n_pages, p->max_pages, p->max_new);
+    if (p->n_tokens < 0) return fail(COBS_ERR_INVALID_ARG, "n_tokens (%d) must be >= 0", p->n_tokens);
+    if (p->R > cobs::kMaxRequests) return fail(COBS_ERR_UNSUPPORTED, "%d requests > %d", p->R, cobs::kMaxRequests);
+    if (p->Hq % p->Hkv != 0) return fail(COBS_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d)", p->Hq, p->Hkv);
+    if (p->Hq / p->Hkv > 16) return fail(COBS_ERR_UNSUPPORTED, "GQA group size %d > 16", p->Hq / p->Hkv);
+    if (p->d != 64 && p->d != 128) return fail(COBS_ERR_UNSUPPORTED, "head dimension %d (supported: 64, 128)", p->d);
+    if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128)
+        return fail(COBS_ERR_UNSUPPORTED, "page of %d tokens (supported: 16, 32, 64, 128)", p->page);
+    if (p->window < 0 || p->sinks < 0)
+        return fail(COBS_ERR_INVALID_ARG, "window (%d) and sinks (%d) must be >= 0", p->window, p->sinks);
+    if (p->sinks > 0 && p->window == 0) return fail(COBS_ERR_INVALID_ARG, "sinks (%d) without a window", p->sinks);
+    if (p->dtype != COBS_F32 && p->dtype != COBS_BF16) return fail(COBS_ERR_INVALID_ARG, "dtype %d", p->dtype);
+    // slots, positions and (page, head) rows are int32
+    if ((long long)p->n_pages * p->page > INT32_MAX || (long long)p->n_pages * p->Hkv > INT32_MAX ||
+        (long long)p->max_pages * p->page > INT32_MAX || (long long)p->n_tokens * p->Hq > INT32_MAX)
+        return fail(COBS_ERR_UNSUPPORTED, "n_pages * page, n_pages * Hkv, max_pages * page or n_tokens * Hq exceeds 2^31 - 1");
+    const long long e = p->dtype == COBS_BF16 ? 2 : 4;
+    const long long qs = p->q_stride, ks = p->kv_stride;
+    if ((qs != 0 && qs < (long long)p->Hq * p->d) || (ks != 0 && ks < (long long)p->Hkv * p->d) || qs * e % 16 != 0 ||
+        ks * e % 16 != 0 || qs > (1ll << 36) || ks > (1ll << 36))
+        return fail(COBS_ERR_INVALID_ARG, "q_stride (%lld) / kv_stride (%lld): 0, or at least a token's elements in 16-byte multiples",
+                    qs, ks);
     return COBS_OK;
 }
 
@@ -402,6 +439,85 @@ cobs_status cobs_query_basis(const cobs_params* p, const void* Q, int64_t n, flo
     if (ws_bytes < need) return fail(COBS_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
     cudaError_t e = cobs::launch_query_basis(mb, Q, (long long)n, basis, eigenvalues, workspace, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "cobs_query_basis launch");
+    return COBS_OK;
+}
+
+size_t cobs_paged_workspace_bytes(const cobs_paged_params* p) {
+    if (validate_paged(p) != COBS_OK) return 0;
+    return cobs::paged_attn_workspace_bytes(cobs::make_paged_dims(*p));
+}
+
+cobs_status cobs_paged_tables(const cobs_paged_params* p, const int32_t* cached_len, const int32_t* new_len,
+                              const int32_t* free_pages, int32_t n_free, const int32_t* free_count,
+                              int32_t* block_table, int32_t* cu_new, int32_t* kv_len, int32_t* slot_map,
+                              int32_t* counts, cobs_stream_t stream) {
+    COBS_TRY(validate_paged(p));
+    if (n_free < 0) return fail(COBS_ERR_INVALID_ARG, "n_free (%d) must be >= 0", n_free);
+    COBS_TRY(check_ints(cached_len, "cached_len"));
+    COBS_TRY(check_ints(new_len, "new_len"));
+    if (n_free > 0) COBS_TRY(check_ints(free_pages, "free_pages"));
+    COBS_TRY(check_ints(free_count, "free_count"));
+    COBS_TRY(check_ints(block_table, "block_table"));
+    COBS_TRY(check_ints(cu_new, "cu_new"));
+    COBS_TRY(check_ints(kv_len, "kv_len"));
+    if (p->n_tokens > 0) COBS_TRY(check_ints(slot_map, "slot_map"));
+    COBS_TRY(check_ints(counts, "counts"));
+    // blocks read the inputs while others write the outputs
+    const struct { const int32_t* at; long long n; const char* name; } in[] = {
+        {cached_len, p->R, "cached_len"}, {new_len, p->R, "new_len"}, {free_pages, n_free, "free_pages"}, {free_count, 1, "free_count"}},
+        out[] = {{block_table, (long long)p->R * p->max_pages, "block_table"}, {cu_new, p->R + 1, "cu_new"}, {kv_len, p->R, "kv_len"},
+                 {slot_map, p->n_tokens, "slot_map"}, {counts, 4, "counts"}};
+    for (const auto& i : in)
+        for (const auto& o : out)
+            if (i.at < o.at + o.n && o.at < i.at + i.n)
+                return fail(COBS_ERR_INVALID_ARG, "%s overlaps %s", i.name, o.name);
+    int* flag = nullptr;
+    COBS_TRY(device_flag(&flag));
+    const cudaError_t e = cobs::launch_paged_tables(cobs::make_paged_dims(*p), cached_len, new_len, free_pages, n_free, free_count,
+                                                    block_table, cu_new, kv_len, slot_map, counts, (cudaStream_t)stream, flag);
+    if (e != cudaSuccess) return cuda_fail(e, "cobs_paged_tables launch");
+    return COBS_OK;
+}
+
+cobs_status cobs_paged_append(const cobs_paged_params* p, const void* K, const void* V, const int32_t* slot_map,
+                              void* k_cache, void* v_cache, cobs_stream_t stream) {
+    COBS_TRY(validate_paged(p));
+    if (p->n_tokens == 0) return COBS_OK;
+    COBS_TRY(check_ptr(K, "K"));
+    COBS_TRY(check_ptr(V, "V"));
+    COBS_TRY(check_ints(slot_map, "slot_map"));
+    COBS_TRY(check_ptr(k_cache, "k_cache"));
+    COBS_TRY(check_ptr(v_cache, "v_cache"));
+    int* flag = nullptr;
+    COBS_TRY(device_flag(&flag));
+    const cudaError_t e = cobs::launch_paged_append(cobs::make_paged_dims(*p), K, V, slot_map, k_cache, v_cache,
+                                                    (cudaStream_t)stream, flag);
+    if (e != cudaSuccess) return cuda_fail(e, "cobs_paged_append launch");
+    return COBS_OK;
+}
+
+cobs_status cobs_paged_attn(const cobs_paged_params* p, const void* Q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* cu_new, const int32_t* kv_len, void* O,
+                            float* lse, void* workspace, size_t ws_bytes, cobs_stream_t stream) {
+    COBS_TRY(validate_paged(p));
+    if (p->n_tokens == 0) return COBS_OK;
+    COBS_TRY(check_ptr(Q, "Q"));
+    COBS_TRY(check_ptr(k_cache, "k_cache"));
+    COBS_TRY(check_ptr(v_cache, "v_cache"));
+    COBS_TRY(check_ints(block_table, "block_table"));
+    COBS_TRY(check_ints(cu_new, "cu_new"));
+    COBS_TRY(check_ints(kv_len, "kv_len"));
+    COBS_TRY(check_ptr(O, "O"));
+    COBS_TRY(check_ptr(lse, "lse", true));
+    COBS_TRY(check_ptr(workspace, "workspace"));
+    const cobs::PagedDims m = cobs::make_paged_dims(*p);
+    const size_t need = cobs::paged_attn_workspace_bytes(m);
+    if (ws_bytes < need) return fail(COBS_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    int* flag = nullptr;
+    COBS_TRY(device_flag(&flag));
+    const cudaError_t e = cobs::launch_paged_attn(m, Q, k_cache, v_cache, block_table, cu_new, kv_len, O, lse, workspace,
+                                                  (cudaStream_t)stream, flag);
+    if (e != cudaSuccess) return cuda_fail(e, "cobs_paged_attn launch");
     return COBS_OK;
 }
 

@@ -1,0 +1,17 @@
+// Kernels behind the paged attention call (internal to the library).
+#pragma once
+
+#include "dims.h"
+#include "paged.h"
+
+namespace cobs {
+
+struct PagedArgs;
+
+// float32 on the CUDA cores: rows of a record, blocks launched.
+int paged_simt_rec_rows(const PagedDims& m);
+int paged_simt_workers(const PagedDims& m);
+cudaError_t launch_paged_simt(const PagedDims& m, const PagedArgs& a, const void* Q, const void* kc,
+                              const void* vc, cudaStream_t s);
+
+}  // namespace cobs

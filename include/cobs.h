@@ -322,6 +322,98 @@ cobs_status cobs_query_basis(const cobs_params* p, const void* Q, int64_t n, flo
 cobs_status cobs_block_log_mass(const cobs_params* p, const void* Q, const void* K, float* out,
                                 cobs_stream_t stream);
 
+/*
+ * Paged KV cache: requests of different lengths whose keys and values lie in pages of one cache,
+ * for the dense and sliding-window layers that stand beside the block-sparse ones ([NSA-181]
+ * sliding-window path; [COBS] "Problemstellung": decoding is bound by the cache reads) and for
+ * programs that serve requests of mixed lengths.
+ *
+ * Layouts (row-major; element type per `dtype`, integers int32, all DEVICE memory):
+ *     k_cache, v_cache  [n_pages, Hkv, page, d]   one page of one head is contiguous
+ *     block_table       [R, max_pages]            page that holds tokens j*page .. of request r
+ *                                                  (-1: none). Pages may be shared by requests.
+ *     K, V  (new rows)  [n_tokens, Hkv, d]        the requests' new tokens one after the other
+ *     Q, O              [n_tokens, Hq, d]
+ *     cu_new            [R + 1]                   first token row of each request; cu_new[R]: rows in use
+ *     kv_len            [R]                       keys of each request, its new tokens included
+ *     slot_map          [n_tokens]                page * page_size + offset of each row, -1: none
+ * Token rows behind the last request's (cu_new[R] .. n_tokens - 1) are padding: they are not read
+ * and their outputs are left as they were. A token's rows of all heads are contiguous; the distance
+ * between tokens is q_stride / kv_stride elements, so Q, K and V may be slices of one fused
+ * projection. Everything that depends on the lengths is read on the device, so the calls can be
+ * captured in a graph and replayed with other lengths.
+ * Lengths that contradict each other, the token rows or the table leave a request out (its rows
+ * stay as they were); such lengths, and page or slot numbers outside the cache, are recorded in the
+ * flag read by cobs_device_error(). */
+typedef struct {
+    int32_t R;          /* requests (1 .. 16384): rows of the block table */
+    int32_t Hq;         /* query heads */
+    int32_t Hkv;        /* key/value heads; Hq / Hkv <= 16 */
+    int32_t d;          /* head dimension, 64 or 128 */
+    int32_t page;       /* tokens per page: 16, 32, 64 or 128 */
+    int32_t n_pages;    /* pages of the cache (n_pages * page and n_pages * Hkv at most 2^31 - 1) */
+    int32_t max_pages;  /* width of the block table */
+    int32_t n_tokens;   /* token rows of Q, K, V, O and slot_map (0: the calls on rows do nothing) */
+    int32_t max_new;    /* no request has more new tokens than this (1: single-token decoding) */
+    int32_t window;     /* 0: every earlier token is visible; W: the last W, the token itself included */
+    int32_t sinks;      /* with a window: the first `sinks` tokens of a request stay visible */
+    int32_t dtype;      /* cobs_dtype of Q, K, V, O and the caches */
+    int64_t q_stride;   /* elements from one token's Q to the next (0: Hq * d); 16-byte multiple */
+    int64_t kv_stride;  /* the same of K and V (0: Hkv * d) */
+} cobs_paged_params;
+
+/*
+ * Tables of one step from the requests' lengths. Request r holds cached_len[r] tokens and gets
+ * new_len[r] more (at most max_new):
+ *   cu_new, kv_len  the running sums of new_len (from 0) and cached_len + new_len;
+ *   block_table     in/out: entries ceil(c / page) .. ceil((c + n) / page) - 1 of row r receive free
+ *                   pages; the others are read where a request's last page is still open, and kept;
+ *   slot_map        row cu_new[r] + i: the slot of position cached_len[r] + i; -1 for padding;
+ *   counts          [4]: token rows in use, pages needed, pages left on the stack, pages missing.
+ * Free pages are free_pages[0 .. free_count[0] - 1] (at most n_free), taken from the top down in the
+ * order of requests and positions; the caller's next step starts from counts[2] pages. When pages
+ * are missing (counts[3] > 0) the entries and slots without a page are -1: the caller drops
+ * requests and calls again before it uses them.
+ * block_table rows, counts and the other outputs must not overlap the inputs. Hq, Hkv, d, window
+ * and dtype are not used (but must be valid).
+ */
+cobs_status cobs_paged_tables(const cobs_paged_params* p, const int32_t* cached_len, const int32_t* new_len,
+                              const int32_t* free_pages, int32_t n_free, const int32_t* free_count,
+                              int32_t* block_table, int32_t* cu_new, int32_t* kv_len, int32_t* slot_map,
+                              int32_t* counts, cobs_stream_t stream);
+
+/*
+ * Append: the K and V row of every token row t with slot_map[t] >= 0 is copied to its slot of the
+ * caches. Slots of one call must be distinct (of two rows with one slot, either may stay, in
+ * 16-byte pieces).
+ */
+cobs_status cobs_paged_append(const cobs_paged_params* p, const void* K, const void* V, const int32_t* slot_map,
+                              void* k_cache, void* v_cache, cobs_stream_t stream);
+
+/*
+ * Attention of every request's new tokens (a chunk of a prompt, a single token, or a mixture) over
+ * its pages: the row of new token i of request r stands at position t = kv_len[r] - n + i, n =
+ * cu_new[r + 1] - cu_new[r], and
+ *   o_h = sum_j p_j v_j / sum_j p_j,  p_j = exp(q_h . k_j / sqrt(d)),
+ * over the keys j <= t of the request with window == 0, or t - j < window, or j < sinks. Products
+ * and sums are float32 (bf16: p is rounded to bf16 for the product with v, the sum is not); o is
+ * rounded once. What a row does not see does not touch it, whatever it holds (slots behind a
+ * request's keys, pages before its window, later tokens of its chunk). A row that sees nothing
+ * (t < 0) gives zeros. A visible page outside the cache counts as zero keys and values and is
+ * recorded.
+ *   lse         NULL, or [n_tokens, Hq] float32: ln sum_j p_j (-infinity for a row that sees nothing).
+ *   workspace   >= cobs_paged_workspace_bytes(p) bytes (sized for the current device's SM count), no
+ *               initial contents. Calls that share one workspace must not run concurrently.
+ * The result does not depend on timing: the work is divided by the lengths alone and partial
+ * results are joined in a fixed order.
+ */
+cobs_status cobs_paged_attn(const cobs_paged_params* p, const void* Q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* cu_new, const int32_t* kv_len, void* O,
+                            float* lse, void* workspace, size_t ws_bytes, cobs_stream_t stream);
+
+/* Bytes of workspace cobs_paged_attn needs (0 for an invalid p). */
+size_t cobs_paged_workspace_bytes(const cobs_paged_params* p);
+
 /* Bytes of workspace a call needs (0 for an invalid p). */
 size_t cobs_workspace_bytes(const cobs_params* p, int32_t which);
 
