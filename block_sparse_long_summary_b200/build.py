@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libcobs.so")
 SOURCES = ["api.cu", "summary.cu", "select.cu", "decode.cu", "decode_stream.cu", "decode_step.cu", "tma.cu", "prefill.cu",
-           "mass.cu", "basis.cu", "paged_tables.cu", "paged_attn.cu", "paged_simt.cu"]
+           "mass.cu", "basis.cu", "paged_tables.cu", "paged_attn.cu", "paged_simt.cu",
+           "paged_chunk.cu"]
 HEADERS = ["common.cuh", "attn.cuh", "dims.h", "tma.h", "tc.cuh", "select_core.cuh", "stream_tile.cuh",
            "paged.h", "paged_kernels.h", "paged_plan.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -17,8 +17,9 @@ struct Layout {
 
 Layout layout_of(const PagedDims& m) {
     Layout l;
-    l.workers = paged_simt_workers(m);
-    l.rec_rows = paged_simt_rec_rows(m);
+    const bool tensor = m.dtype == COBS_BF16;
+    l.workers = tensor ? paged_chunk_workers(m) : paged_simt_workers(m);
+    l.rec_rows = tensor ? paged_chunk_rec_rows(m) : paged_simt_rec_rows(m);
     l.seg_bytes = al256((size_t)l.workers * sizeof(int4));
     l.rec_bytes = (size_t)l.workers * 2 * l.rec_rows * (m.d + 4) * sizeof(float);
     return l;
@@ -45,7 +46,8 @@ cudaError_t launch_paged_attn(const PagedDims& m, const void* Q, const void* k_c
     a.n_pages = m.n_pages; a.max_pages = m.max_pages; a.n_tokens = m.n_tokens; a.max_new = m.max_new;
     a.W = m.W; a.S = m.S;
     a.sl2 = (float)(1.4426950408889634 / sqrt((double)m.d));
-    return launch_paged_simt(m, a, Q, k_cache, v_cache, s);
+    if (m.dtype == COBS_BF16) return launch_paged_chunk(m, a, Q, k_cache, v_cache, s);
+    return launch_paged_simt(m, a, static_cast<const float*>(Q), static_cast<const float*>(k_cache), static_cast<const float*>(v_cache), s);
 }
 
 }  // namespace cobs

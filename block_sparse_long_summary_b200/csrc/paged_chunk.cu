@@ -1,0 +1,542 @@
+// Attention of new tokens over a paged cache on the fifth-generation tensor cores (tcgen05, TMEM), bf16.
+//
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(q . k_j / sqrt(d)),  over the keys j <= t visible at
+//   the row's position t (all of them, or the last W and the first S).
+//
+// One persistent CTA per SM walks its range of (unit, 128-key tile) pairs (paged_plan.cuh). A unit's
+// rows are two MMA tiles of 128: each holds floor(128 / G) tokens x the G heads of the group, so K
+// and V are read once per group and a tile spans few positions. Per key tile and row tile g:
+//   S_g = Q_g K^T           tcgen05.mma, M 128, N 128, K d, into 128 TMEM columns
+//   p = 2^(s c - m)         one thread per row: the row in registers, no exchange between threads;
+//                           m moves only when a row's maximum grows by more than 2^8 (then the
+//                           thread rescales its row of O, which is seldom)
+//   O_g += P_g V            P in bf16 over S's columns (A operand from TMEM), V MN-major
+// The two row tiles alternate: while the tensor pipe runs P V of one and the next Q K^T of it, the
+// other one's softmax runs. MMAs are issued by one thread in the order PV_0(k) QK_0(k+1) PV_1(k)
+// QK_1(k+1): the pipe runs them in order, so S_g(k+1) arriving means that P_g(k) has been read and
+// O_g is up to date, and no barrier is needed for either.
+// Roles: warps 0-3 and 4-7 softmax and epilogue of row tiles 0 and 1; warp 8 loads (one TMA box per
+// page and 64 columns; pages no row needs come as out-of-range boxes, that is zeros); warp 9 issues
+// the MMAs; warps 10 and 11 prepare V of the tiles that some row does not see in full: rows of V no
+// row of the unit sees (slots behind the keys, keys before the window: any bits) are set to zero,
+// since 0 * NaN would reach O, and the others are looked over for infinities and NaN: such a tile's
+// product is formed by the softmax threads, key by key, so that only the rows that see them change.
+// Every wait is bounded; one that gives up sets the device error flag and the CTA winds down.
+#include <algorithm>
+
+#include "paged.h"
+#include "paged_kernels.h"
+#include "paged_plan.cuh"
+#include "tc.cuh"
+#include "tma.h"
+
+namespace cobs {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kKT = 128;      // keys per tile
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10;
+constexpr int kFixDepth = 4;    // tiles whose V may be prepared ahead of their products
+constexpr uint32_t kBox = 128 * 128;  // 128 rows of 64 columns
+constexpr uint32_t kColO = 256;       // S_g (and P_g) at 128 g, O_g at 256 + 128 g
+
+template <int D>
+struct Cfg {
+    static constexpr int H = D / 64;                  // 64-column halves
+    static constexpr uint32_t kTile = H * kBox;       // a row tile of Q, a key tile of K or V
+    static constexpr int kStages = D == 128 ? 5 : 8;  // K and V tiles in flight
+    static constexpr uint32_t kSmem = 1024 + (2 + kStages) * kTile;
+    static constexpr uint32_t kIdescS = tc::idesc_bf16(128, kKT, 0, 0);
+    static constexpr uint32_t kIdescPV = tc::idesc_bf16(128, D, 0, 1);
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// 32 columns into s[base ..], without waiting
+template <int BASE>
+__device__ __forceinline__ void ld32_at(uint32_t taddr, float (&s)[kKT]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(s[BASE + 0]), "=f"(s[BASE + 1]), "=f"(s[BASE + 2]), "=f"(s[BASE + 3]), "=f"(s[BASE + 4]), "=f"(s[BASE + 5]),
+          "=f"(s[BASE + 6]), "=f"(s[BASE + 7]), "=f"(s[BASE + 8]), "=f"(s[BASE + 9]), "=f"(s[BASE + 10]), "=f"(s[BASE + 11]),
+          "=f"(s[BASE + 12]), "=f"(s[BASE + 13]), "=f"(s[BASE + 14]), "=f"(s[BASE + 15]), "=f"(s[BASE + 16]), "=f"(s[BASE + 17]),
+          "=f"(s[BASE + 18]), "=f"(s[BASE + 19]), "=f"(s[BASE + 20]), "=f"(s[BASE + 21]), "=f"(s[BASE + 22]), "=f"(s[BASE + 23]),
+          "=f"(s[BASE + 24]), "=f"(s[BASE + 25]), "=f"(s[BASE + 26]), "=f"(s[BASE + 27]), "=f"(s[BASE + 28]), "=f"(s[BASE + 29]),
+          "=f"(s[BASE + 30]), "=f"(s[BASE + 31])
+        : "r"(taddr));
+}
+// After wait_ld: the 32 registers are not to be used before this point.
+__device__ __forceinline__ void touch32(float (&s)[kKT], const int base) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(s[base + j]));
+}
+__device__ __forceinline__ float ld1(uint32_t taddr) {
+    float v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr));
+    return v;
+}
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+struct ChunkMaps {
+    CUtensorMap q, k, v;
+};
+
+// A tile some row of the unit does not see in full.
+__device__ __forceinline__ bool masked_tile(const PagedArgs& a, const PagedEntry& e, int j0) {
+    return !(j0 + kKT - 1 <= e.pos0 && (a.W <= 0 || e.last_pos() - j0 < a.W));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, PagedArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ __align__(8) uint64_t barQ, barQfree, barKV[C::kStages], barFree[C::kStages], barS[2], barP[2], barO[2], barFix[kFixDepth], barDone;
+    __shared__ uint32_t tmem_sh;
+    __shared__ int dirty_sh[kFixDepth][2];
+    __shared__ long long tmp[kThreads / 32];
+    __shared__ PagedRange range;
+    unsigned char* sQ = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* sKV = sQ + 2 * C::kTile;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int TM = 128 / a.G, TQ = 2 * TM;  // tokens of a row tile and of a unit
+    if (warp == 0) {
+        tc::tmem_alloc(&tmem_sh, 512);
+        tc::tmem_relinquish();
+    }
+    if (tid == 32) {
+        mbar_init(&barQ, 1);
+        mbar_init(&barQfree, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&barKV[s], 1);
+            mbar_init(&barFree[s], 3);  // the MMAs that read it, and the two V warps
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&barS[g], 1);
+            mbar_init(&barP[g], 4);
+            mbar_init(&barO[g], 1);
+        }
+        for (int f = 0; f < kFixDepth; ++f) mbar_init(&barFix[f], 2);
+        mbar_init(&barDone, 1);
+        fence_barrier_init();
+    }
+    plan_ranges<kThreads, kKT, 1>(a, TQ, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sKV), tmp, &range);
+    if (tid == 0) a.seg[blockIdx.x] = make_int4(range.r, range.i, range.off, range.count);
+    fence_proxy_async();  // the plan's use of the ring before TMA's
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const PagedRange rg = range;
+    const uint32_t tmem = tmem_sh;
+    bool ok = true;
+    PagedWalk<kKT> w;
+    bool more = w.first(a, TQ, rg);
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax and epilogue of row tile g
+        reg_inc<216>();
+        const int g = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + 128 * g, tO = tmem + lanes + kColO + 128 * g;
+        const int tok = row / a.G, hrow = row - tok * a.G;
+        const float sl2 = a.sl2;
+        uint32_t nS = 0, nO = 0, nFix = 0;
+        int piece = 0;
+        for (; more && ok; more = w.next(a, TQ), ++piece) {
+            const PagedEntry& e = w.e;
+            const bool mine = g == 0 || e.n > TM;  // the unit has this row tile
+            const int ntok = min(TM, e.n - g * TM);
+            const bool live = mine && tok < ntok;
+            const bool warp_live = mine && (warp & 3) * 32 < ntok * a.G;
+            const int t = e.pos0 + g * TM + tok;
+            float m = -INFINITY, l = 0.0f;
+            for (int k = w.t0; k < w.t1; ++k) {
+                const int j0 = e.key_tile(k) * kKT;
+                const bool masked = masked_tile(a, e, j0);
+                const uint32_t fix = nFix;
+                nFix += masked;
+                if (!mine) continue;
+                if (ok) ok = mbar_wait(&barS[g], nS & 1, a.err);
+                ++nS;
+                int dirty = 0;  // the stage of V (from 1) where this thread forms the product
+                if (masked && ok) {  // (after S: the tiles before this one have then been prepared)
+                    ok = mbar_wait(&barFix[fix % kFixDepth], (fix / kFixDepth) & 1, a.err);
+                    dirty = max(dirty_sh[fix % kFixDepth][0], dirty_sh[fix % kFixDepth][1]);
+                }
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (warp_live) {
+                    float s[kKT];
+                    ld32_at<0>(tS, s);
+                    ld32_at<32>(tS + 32, s);
+                    ld32_at<64>(tS + 64, s);
+                    ld32_at<96>(tS + 96, s);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int c = 0; c < kKT; c += 32) touch32(s, c);
+                    const int hi = t - j0, lo = a.W > 0 ? hi - a.W + 1 : 0, sk = a.W > 0 ? a.S - j0 : 0;
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < kKT; ++j) s[j] = (j <= hi && (j >= lo || j < sk)) ? s[j] : -INFINITY;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int j = 0; j < kKT; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                    const bool grow = mt > m + 8.0f;  // (from -infinity too; never for a row that sees nothing)
+                    if (k > w.t0 && __any_sync(kFull, grow && m != -INFINITY)) {
+                        const float f = grow ? tc::ex2(m - mt) : 1.0f;
+                        l *= f;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tc::ld32(tO + c, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] *= f;
+                            tc::st32(tO + c, o);
+                        }
+                        tc::wait_st();
+                    }
+                    if (grow) m = mt;
+                    const float neg = m == -INFINITY ? 0.0f : -m;
+                    float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float x0 = tc::ex2(fmaf(s[32 * c + 2 * j], sl2, neg)), x1 = tc::ex2(fmaf(s[32 * c + 2 * j + 1], sl2, neg));
+                            s[32 * c + 2 * j] = x0;
+                            s[32 * c + 2 * j + 1] = x1;
+                            ps[j & 3] += x0 + x1;
+                            pk[j] = pack_bf16(x0, x1);
+                        }
+                        if (!dirty) st16(tS + 16 * c, pk);
+                    }
+                    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                    tc::wait_st();
+                    if (dirty) {
+                        // P V by this row's thread: p in bf16 as the tensor cores take it (over S), V from the ring
+#pragma unroll
+                        for (int c = 0; c < kKT; c += 32) {
+                            float p[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) p[j] = __bfloat162float(__float2bfloat16_rn(s[c + j]));
+                            tc::st32(tS + c, p);
+                        }
+                        tc::wait_st();
+                        const unsigned char* sV = sKV + (size_t)(dirty - 1) * C::kTile;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            if (k > w.t0) {
+                                tc::ld32(tO + c, o);
+                                tc::wait_ld();
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+                            }
+#pragma unroll 1
+                            for (int j = 0; j < kKT; ++j) {
+                                const float p = ld1(tS + j);
+                                tc::wait_ld();
+                                const bool see = j <= hi && (j >= lo || j < sk);
+                                const unsigned char* vr = sV + (c >> 6) * kBox + j * 128;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(vr + (((((c & 63) >> 3) + q) ^ (j & 7)) << 4));
+                                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) {
+                                        o[8 * q + 2 * y] = see ? fmaf(p, __uint_as_float(x[y] << 16), o[8 * q + 2 * y]) : o[8 * q + 2 * y];
+                                        o[8 * q + 2 * y + 1] =
+                                            see ? fmaf(p, __uint_as_float(x[y] & 0xffff0000u), o[8 * q + 2 * y + 1]) : o[8 * q + 2 * y + 1];
+                                    }
+                                }
+                            }
+                            tc::st32(tO + c, o);
+                        }
+                        tc::wait_st();
+                    }
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&barP[g]);
+            }
+            if (!mine) continue;
+            if (ok) ok = mbar_wait(&barO[g], nO & 1, a.err);
+            ++nO;
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (!warp_live) continue;
+            const size_t orow = (size_t)(e.row0 + g * TM + (live ? tok : 0)) * a.Hq + w.h * a.G + (live ? hrow : 0);
+            if (w.whole()) {
+                const bool empty = t < 0;
+                const float inv = empty ? 0.0f : 1.0f / l;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.O) + orow * D;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tc::ld32(tO + c, o);
+                    tc::wait_ld();
+                    if (live) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint4 v;
+                            v.x = pack_bf16(o[j] * inv, o[j + 1] * inv);
+                            v.y = pack_bf16(o[j + 2] * inv, o[j + 3] * inv);
+                            v.z = pack_bf16(o[j + 4] * inv, o[j + 5] * inv);
+                            v.w = pack_bf16(o[j + 6] * inv, o[j + 7] * inv);
+                            *reinterpret_cast<uint4*>(out + c + j) = empty ? make_uint4(0u, 0u, 0u, 0u) : v;
+                        }
+                    }
+                }
+                if (live && a.lse) a.lse[orow] = empty ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            } else {
+                float* rec = a.rec + (((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * (TQ * a.G) + (g * TM + tok) * a.G + hrow) * (D + 4);
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tc::ld32(tO + c, o);
+                    tc::wait_ld();
+                    if (live) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4*>(rec + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
+                }
+                if (live) {
+                    rec[D] = m;
+                    rec[D + 1] = l;
+                }
+            }
+        }
+    } else {
+        reg_dec<72>();
+        if (warp == kLoadWarp) {
+            // -------------------------------------------------------- loads
+            const int ppt = kKT >> a.page_shift, per = 32 / ppt;  // pages per tile, tiles per look-up of 32 entries
+            const uint32_t zero_box = (uint32_t)a.n_pages * a.Hkv;
+            uint32_t n = 0, u = 0;
+            for (; more && ok; more = w.next(a, TQ), ++u) {
+                const PagedEntry& e = w.e;
+                const int hi = e.last_pos();
+                const bool two = e.n > TM;
+                auto first_key = [&](int k0) { return k0 + lane / ppt < w.t1 ? (e.key_tile(k0 + lane / ppt) * kKT + ((lane % ppt) << a.page_shift)) : -1; };
+                auto entry = [&](int k0) {  // raw table entry of this lane's page
+                    const int j = first_key(k0), slot = j >> a.page_shift;
+                    return j >= 0 && j <= hi && slot < a.max_pages && (j + a.page > e.lo || j < a.S)
+                               ? __ldg(a.table + (size_t)e.r * a.max_pages + slot) : INT_MIN;
+                };
+                int raw = entry(w.t0), k0 = w.t0;
+                uint32_t z = 0;
+                for (int k = w.t0; k < w.t1 && ok; ++k) {
+                    if (k == w.t0 || k == k0 + per) {
+                        if (k != w.t0) k0 = k;
+                        // pages no row needs, and (recorded) those outside the cache, read as zeros
+                        const bool in = raw >= 0 && raw < a.n_pages;
+                        if (!in && raw != INT_MIN) report_error(a.err, kErrBadIndex);
+                        z = in ? (uint32_t)raw * a.Hkv + w.h : zero_box;
+                        raw = entry(k0 + per);
+                    }
+                    const uint32_t zt = __shfl_sync(kFull, z, (k - k0) * ppt + (lane & (ppt - 1)));
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++n) {
+                        const uint32_t s = n % C::kStages;
+                        if (n >= C::kStages && ok) ok = mbar_wait(&barFree[s], ((n / C::kStages) - 1) & 1, a.err);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&barKV[s], C::kTile);
+                        __syncwarp();
+                        if (lane < ppt) {
+                            unsigned char* dst = sKV + (size_t)s * C::kTile + (lane << a.page_shift) * 128;
+#pragma unroll
+                            for (int h = 0; h < C::H; ++h)
+                                tma_load_3d(dst + h * kBox, kv == 0 ? &maps.k : &maps.v, 64 * h, 0, (int)zt, &barKV[s]);
+                        }
+                    }
+                    if (k == w.t0 && ok) {
+                        if (u > 0) ok = mbar_wait(&barQfree, (u - 1) & 1, a.err);
+                        if (ok && lane == 0) {
+                            mbar_arrive_expect_tx(&barQ, (two ? 2 : 1) * C::H * a.G * TM * 128);
+                            for (int g = 0; g < (two ? 2 : 1); ++g)
+                                for (int h = 0; h < C::H; ++h)
+                                    tma_load_3d(sQ + g * C::kTile + h * kBox, &maps.q, 64 * h, w.h * a.G, e.row0 + g * TM, &barQ);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            // wait for the copies that no one consumed (only after a wait that gave up)
+            if (!ok)
+                for (uint32_t s = 0; s < C::kStages && s < n; ++s) mbar_wait(&barKV[s], ((n - 1 - s) / C::kStages) & 1, a.err);
+        } else if (warp == kMmaWarp) {
+            // -------------------------------------------------------- tensor cores
+            const uint32_t q_addr = smem_addr(sQ), kv_addr = smem_addr(sKV);
+            uint32_t n = 0, u = 0, nFix = 0, nP[2] = {0, 0};
+            auto wait_stage = [&](uint32_t i) { if (ok) ok = mbar_wait(&barKV[i % C::kStages], (i / C::kStages) & 1, a.err); };
+            auto qk = [&](int g, uint32_t i) {
+                const uint32_t kb = kv_addr + (i % C::kStages) * C::kTile, qb = q_addr + g * C::kTile;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc::mma_f16_ss(tmem + 128 * g, tc::smem_desc_sw128(qb + (ks >> 2) * kBox + (ks & 3) * 32, 16, 1024),
+                                   tc::smem_desc_sw128(kb + (ks >> 2) * kBox + (ks & 3) * 32, 16, 1024), C::kIdescS, ks > 0);
+                tc::commit(&barS[g]);
+            };
+            for (; more && ok; more = w.next(a, TQ), ++u) {
+                const PagedEntry& e = w.e;
+                const int nb = e.n > TM ? 2 : 1;
+                if (ok) ok = mbar_wait(&barQ, u & 1, a.err);
+                wait_stage(n);
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    for (int g = 0; g < nb; ++g) qk(g, n);
+                    tc::commit(&barFree[n % C::kStages]);
+                    if (w.t1 - w.t0 == 1) tc::commit(&barQfree);
+                }
+                for (int k = w.t0; k < w.t1 && ok; ++k, n += 2) {
+                    const bool last = k + 1 == w.t1;
+                    bool dirty = false;
+                    if (!last) wait_stage(n + 2);
+                    wait_stage(n + 1);
+                    if (masked_tile(a, e, e.key_tile(k) * kKT)) {
+                        if (ok) ok = mbar_wait(&barFix[nFix % kFixDepth], (nFix / kFixDepth) & 1, a.err);
+                        dirty = (dirty_sh[nFix % kFixDepth][0] | dirty_sh[nFix % kFixDepth][1]) != 0;
+                        ++nFix;
+                    }
+                    const uint32_t vb = kv_addr + ((n + 1) % C::kStages) * C::kTile;
+                    for (int g = 0; g < nb && ok; ++g) {
+                        ok = mbar_wait(&barP[g], nP[g] & 1, a.err);
+                        ++nP[g];
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        if (lane == 0) {
+                            if (!dirty) {
+#pragma unroll
+                                for (int kk = 0; kk < kKT / 16; ++kk)
+                                    mma_f16_ts(tmem + kColO + 128 * g, tmem + 128 * g + 8 * kk,
+                                               tc::smem_desc_sw128(vb + kk * 16 * 128, kBox, 1024), C::kIdescPV, k > w.t0 || kk > 0);
+                            }
+                            if (g == nb - 1) tc::commit(&barFree[(n + 1) % C::kStages]);
+                            if (last) {
+                                tc::commit(&barO[g]);
+                            } else {
+                                qk(g, n + 2);
+                                if (g == nb - 1) {
+                                    tc::commit(&barFree[(n + 2) % C::kStages]);
+                                    if (k + 2 == w.t1) tc::commit(&barQfree);
+                                }
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (lane == 0) {  // the issuing thread stays until its MMAs are done
+                tc::commit(&barDone);
+                mbar_wait(&barDone, 0, a.err);
+            }
+        } else {
+            // -------------------------------------------------------- V of the masked tiles
+            // They pass every stage of the ring (and hand it back with the MMAs), so that they can
+            // neither run ahead of it nor fall behind it.
+            uint32_t n = 0, nFix = 0;
+            const int f = tid - kFixWarp * 32;  // 0 .. 63
+            for (; more && ok; more = w.next(a, TQ)) {
+                const PagedEntry& e = w.e;
+                const int hi = e.last_pos();
+                for (int k = w.t0; k < w.t1 && ok; ++k, n += 2) {
+                    const int j0 = e.key_tile(k) * kKT;
+                    const uint32_t sk = n % C::kStages, s = (n + 1) % C::kStages;
+                    ok = mbar_wait(&barKV[sk], (n / C::kStages) & 1, a.err);
+                    if (ok && lane == 0) mbar_arrive(&barFree[sk]);
+                    if (ok) ok = mbar_wait(&barKV[s], ((n + 1) / C::kStages) & 1, a.err);
+                    if (!ok) break;
+                    if (masked_tile(a, e, j0)) {
+                        unsigned char* sV = sKV + (size_t)s * C::kTile;
+                        bool odd = false;
+#pragma unroll 4
+                        for (int c = f; c < C::H * 128 * 8; c += 64) {
+                            const int j = j0 + ((c >> 3) & 127);
+                            uint4* at = reinterpret_cast<uint4*>(sV + (size_t)c * 16);
+                            if (j <= hi && (j >= e.lo || j < a.S)) {
+                                const uint4 v = *at;
+                                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    odd |= (x[y] & 0x7f80u) == 0x7f80u || (x[y] & 0x7f800000u) == 0x7f800000u;
+                            } else {
+                                *at = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        }
+                        fence_proxy_async();
+                        odd = __any_sync(kFull, odd);
+                        __syncwarp();
+                        if (lane == 0) {
+                            // (kFixDepth tiles on, the readers of this flag have passed: the ring holds fewer)
+                            dirty_sh[nFix % kFixDepth][warp - kFixWarp] = odd ? (int)s + 1 : 0;
+                            mbar_arrive(&barFix[nFix % kFixDepth]);
+                        }
+                        ++nFix;
+                    }
+                    if (lane == 0) mbar_arrive(&barFree[s]);
+                }
+            }
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t run(const PagedDims& m, const PagedArgs& a, const void* Q, const void* kc, const void* vc, cudaStream_t s) {
+    using C = Cfg<D>;
+    const int TM = 128 / m.G, workers = sm_count();
+    ChunkMaps maps;
+    const uint64_t qd[3] = {(uint64_t)D, (uint64_t)m.Hq, (uint64_t)m.n_tokens}, qs[2] = {(uint64_t)D * 2, (uint64_t)m.q_stride * 2};
+    const uint32_t qb[3] = {64, (uint32_t)m.G, (uint32_t)TM};
+    const uint64_t cd[3] = {(uint64_t)D, (uint64_t)m.page, (uint64_t)m.n_pages * m.Hkv}, cs[2] = {(uint64_t)D * 2, (uint64_t)m.page * D * 2};
+    const uint32_t cb[3] = {64, (uint32_t)m.page, 1};
+    if (!encode_tmap_bf16_3d(&maps.q, Q, qd, qs, qb) || !encode_tmap_bf16_3d(&maps.k, kc, cd, cs, cb) ||
+        !encode_tmap_bf16_3d(&maps.v, vc, cd, cs, cb))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    count_launch();
+    paged_chunk_kernel<D><<<workers, kThreads, C::kSmem, s>>>(maps, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_paged_merge<__nv_bfloat16, D, kKT>(a, 2 * TM, workers, 2 * TM * m.G, s);
+}
+
+}  // namespace
+
+int paged_chunk_rec_rows(const PagedDims& m) { return 128 / m.G * 2 * m.G; }
+int paged_chunk_workers(const PagedDims&) { return sm_count(); }
+
+cudaError_t launch_paged_chunk(const PagedDims& m, const PagedArgs& a, const void* Q, const void* kc, const void* vc,
+                               cudaStream_t s) {
+    return m.d == 64 ? run<64>(m, a, Q, kc, vc, s) : run<128>(m, a, Q, kc, vc, s);
+}
+
+}  // namespace cobs

@@ -14,6 +14,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "dims.h"
 
 namespace cobs {
 
@@ -234,6 +235,7 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int r, int slot, bool
 // one warp each. Records lie in the order of the workers, so the sum's order is fixed.
 template <typename T, int D, int KT>
 __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int TQ, int n_workers, int rec_rows) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x + 1;
     const int4 s = a.seg[c];
     if (s.w == 0) return;
@@ -284,6 +286,24 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int TQ, i
             Elem<T>::store(static_cast<T*>(a.O) + orow * D + lane * C + k, empty ? 0.0f : o[k] * inv);
         if (a.lse && lane == 0) a.lse[orow] = empty ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
     }
+}
+
+// The merge after an attention grid of `workers` ranges, as its programmatic dependent (its launch
+// overlaps the grid's tail).
+template <typename T, int D, int KT>
+cudaError_t launch_paged_merge(const PagedArgs& a, int TQ, int workers, int rec_rows, cudaStream_t s) {
+    if (workers < 2) return cudaSuccess;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(workers - 1, (rec_rows + 15) / 16);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, KT>, a, TQ, workers, rec_rows);
 }
 
 }  // namespace cobs

@@ -28,16 +28,6 @@ __device__ __forceinline__ void cp16(void* dst, const void* src, bool ok) {
                  : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void put4(float* dst, const float* src, bool ok) { cp16(dst, src, ok); }
-__device__ __forceinline__ void put4(float* dst, const __nv_bfloat16* src, bool ok) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ok) {
-        const uint2 u = *reinterpret_cast<const uint2*>(src);
-        v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                        __uint_as_float(u.y & 0xffff0000u));
-    }
-    *reinterpret_cast<float4*>(dst) = v;
-}
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int D, int M>
@@ -45,9 +35,9 @@ constexpr size_t simt_smem() {
     return sizeof(float) * ((size_t)M * (D + 4) + (size_t)kKT * (D + 4) + (size_t)kKT * D + (size_t)M * kPS);
 }
 
-template <typename T, int D, int M>
-__global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const T* Q, long long q_stride,
-                                                        const T* kc, const T* vc) {
+template <int D, int M>
+__global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const float* Q, long long q_stride,
+                                                        const float* kc, const float* vc) {
     extern __shared__ __align__(16) float sm[];
     __shared__ long long tmp[kT / 32];
     __shared__ PagedRange range;
@@ -75,14 +65,14 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const T* Q,
             }
         };
         // one tile of K or V: rows no position of the unit sees are zero
-        auto load = [&](float* dst, int stride, const T* cache, int k) {
+        auto load = [&](float* dst, int stride, const float* cache, int k) {
             const int j0 = e.key_tile(k) * kKT;
             for (int c = tid; c < kKT * D / 4; c += kT) {
                 const int row = c / (D / 4), col = c % (D / 4) * 4, j = j0 + row;
                 const int page = page_sh[k & 1][ppt ? row >> a.page_shift : 0];
                 const bool ok = page >= 0 && j <= hi && (j >= e.lo || j < a.S);
                 const size_t at = (((size_t)(ok ? page : 0) * a.Hkv + w.h) * a.page + (j & (a.page - 1))) * D + col;
-                put4(dst + row * stride + col, cache + at, ok);
+                cp16(dst + row * stride + col, cache + at, ok);
             }
         };
         __syncthreads();  // the last unit's (or the plan's) shared memory is free
@@ -90,8 +80,8 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const T* Q,
         for (int c = tid; c < M * D / 4; c += kT) {
             const int row = c / (D / 4), col = c % (D / 4) * 4;
             const bool ok = row < rows;
-            const T* q = Q + (ok ? (size_t)(e.row0 + row / a.G) * q_stride + (size_t)(w.h * a.G + row % a.G) * D : 0);
-            put4(sQ + row * KS + col, q + col, ok);
+            const float* q = Q + (ok ? (size_t)(e.row0 + row / a.G) * q_stride + (size_t)(w.h * a.G + row % a.G) * D : 0);
+            cp16(sQ + row * KS + col, q + col, ok);
         }
         __syncthreads();
         load(sK, KS, kc, w.t0);
@@ -195,13 +185,12 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const T* Q,
             for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
             const int row = ty + 16 * y;
             if (row >= rows) continue;
-            float* dst = nullptr;
-            T* out = nullptr;
+            float* dst;
             float f = 1.0f;
             if (whole) {
                 const size_t orow = (size_t)(e.row0 + row / a.G) * a.Hq + w.h * a.G + row % a.G;
                 const bool empty = pos[y] < 0;
-                out = static_cast<T*>(a.O) + orow * D;
+                dst = static_cast<float*>(a.O) + orow * D;
                 f = empty ? 0.0f : 1.0f / sum;
                 if (a.lse && tx == 0) a.lse[orow] = empty ? -INFINITY : (m[y] + log2f(sum)) * 0.6931471805599453f;
             } else {
@@ -212,26 +201,23 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const T* Q,
                 }
             }
 #pragma unroll
-            for (int x = 0; x < CD; ++x) {
-                const int col = (x / 4) * 64 + tx * 4 + x % 4;
-                if (whole) Elem<T>::store(out + col, o[y][x] * f); else dst[col] = o[y][x];
-            }
+            for (int x = 0; x < CD; x += 4)
+                *reinterpret_cast<float4*>(dst + (x / 4) * 64 + tx * 4) =
+                    make_float4(o[y][x] * f, o[y][x + 1] * f, o[y][x + 2] * f, o[y][x + 3] * f);
         }
     }
 }
 
-template <typename T, int D, int M>
-cudaError_t run(const PagedArgs& a, int workers, const T* Q, long long q_stride, const T* kc, const T* vc,
+template <int D, int M>
+cudaError_t run(const PagedArgs& a, int workers, const float* Q, long long q_stride, const float* kc, const float* vc,
                 cudaStream_t s) {
     const size_t smem = std::max(simt_smem<D, M>(), (size_t)(a.R + 1) * sizeof(int));
-    cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<T, D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    paged_simt_kernel<T, D, M><<<workers, kT, smem, s>>>(a, Q, q_stride, kc, vc);
+    paged_simt_kernel<D, M><<<workers, kT, smem, s>>>(a, Q, q_stride, kc, vc);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (workers > 1)
-        paged_merge_kernel<T, D, kKT><<<dim3(workers - 1, M / 16), 128, 0, s>>>(a, M / a.G, workers, M);
-    return cudaGetLastError();
+    return launch_paged_merge<float, D, kKT>(a, M / a.G, workers, M, s);
 }
 
 }  // namespace
@@ -242,21 +228,13 @@ static int simt_rows(const PagedDims& m) { return (long long)m.max_new * m.G <= 
 int paged_simt_rec_rows(const PagedDims& m) { return simt_rows(m); }
 int paged_simt_workers(const PagedDims& m) { return sm_count() * (simt_rows(m) == 16 ? 2 : 1); }
 
-template <typename T>
-static cudaError_t launch_t(const PagedDims& m, const PagedArgs& a, const T* Q, const T* kc, const T* vc, cudaStream_t s) {
+cudaError_t launch_paged_simt(const PagedDims& m, const PagedArgs& a, const float* Q, const float* kc,
+                              const float* vc, cudaStream_t s) {
     const int n = paged_simt_workers(m);
     const bool few = simt_rows(m) == 16;
-    count_launch(n > 1 ? 2 : 1);
-    if (m.d == 64) return few ? run<T, 64, 16>(a, n, Q, m.q_stride, kc, vc, s) : run<T, 64, 64>(a, n, Q, m.q_stride, kc, vc, s);
-    return few ? run<T, 128, 16>(a, n, Q, m.q_stride, kc, vc, s) : run<T, 128, 64>(a, n, Q, m.q_stride, kc, vc, s);
-}
-
-cudaError_t launch_paged_simt(const PagedDims& m, const PagedArgs& a, const void* Q, const void* kc,
-                              const void* vc, cudaStream_t s) {
-    if (m.dtype == COBS_BF16)
-        return launch_t(m, a, static_cast<const __nv_bfloat16*>(Q), static_cast<const __nv_bfloat16*>(kc),
-                        static_cast<const __nv_bfloat16*>(vc), s);
-    return launch_t(m, a, static_cast<const float*>(Q), static_cast<const float*>(kc), static_cast<const float*>(vc), s);
+    count_launch();
+    if (m.d == 64) return few ? run<64, 16>(a, n, Q, m.q_stride, kc, vc, s) : run<64, 64>(a, n, Q, m.q_stride, kc, vc, s);
+    return few ? run<128, 16>(a, n, Q, m.q_stride, kc, vc, s) : run<128, 64>(a, n, Q, m.q_stride, kc, vc, s);
 }
 
 }  // namespace cobs
