@@ -14,7 +14,9 @@
 // The two row tiles alternate: while the tensor pipe runs P V of one and the next Q K^T of it, the
 // other one's softmax runs. MMAs are issued by one thread in the order PV_0(k) QK_0(k+1) PV_1(k)
 // QK_1(k+1): the pipe runs them in order, so S_g(k+1) arriving means that P_g(k) has been read and
-// O_g is up to date, and no barrier is needed for either.
+// O_g is up to date, and no barrier is needed for either. A unit of one row tile (single tokens,
+// short chunks) gives both halves of the machine to it: the two groups take its key tiles in turn,
+// each with an accumulator and maxima of its own, joined at the unit's end.
 // Roles: warps 0-3 and 4-7 softmax and epilogue of row tiles 0 and 1; warp 8 loads (one TMA box per
 // page and 64 columns; pages no row needs come as out-of-range boxes, that is zeros); warp 9 issues
 // the MMAs; warps 10 and 11 prepare V of the tiles that some row does not see in full: rows of V no
@@ -90,8 +92,51 @@ __device__ __forceinline__ float ld1(uint32_t taddr) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr));
     return v;
 }
+// The two warps (one of each group) that hold the same rows.
+__device__ __forceinline__ void pair_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory"); }
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Bounded wait without a suspend hint: with one, a poll of a phase that is already complete costs 46
+// cycles, without 15 (clock64 around completed phases), and most waits here find theirs complete.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 0; i < kMaxWaitIters; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (global_ns() - t0 > kWaitLimitNs) break;
+    }
+    report_error(err, kErrWaitTimeout);
+    return false;
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)), "l"(reinterpret_cast<uint64_t&>(z)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
+    return r;
+}
 
 struct ChunkMaps {
     CUtensorMap q, k, v;
@@ -111,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     __shared__ int dirty_sh[kFixDepth][2];
     __shared__ long long tmp[kThreads / 32];
     __shared__ PagedRange range;
+    __shared__ float2 ml_sh[128];  // a pair's maxima and sums
     unsigned char* sQ = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char* sKV = sQ + 2 * C::kTile;
 
@@ -160,23 +206,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         int piece = 0;
         for (; more && ok; more = w.next(a, TQ), ++piece) {
             const PagedEntry& e = w.e;
-            const bool mine = g == 0 || e.n > TM;  // the unit has this row tile
-            const int ntok = min(TM, e.n - g * TM);
-            const bool live = mine && tok < ntok;
-            const bool warp_live = mine && (warp & 3) * 32 < ntok * a.G;
-            const int t = e.pos0 + g * TM + tok;
+            const bool pair = e.n <= TM;              // one row tile: the groups take its key tiles in turn
+            const int tok0 = pair ? 0 : g * TM;       // first token of this group's rows
+            const int ntok = min(TM, e.n - tok0);
+            const bool live = tok < ntok;
+            const bool warp_live = (warp & 3) * 32 < ntok * a.G;
+            const int t = e.pos0 + tok0 + tok;
             float m = -INFINITY, l = 0.0f;
+            const int kg = w.t0 + (pair ? g : 0);  // this group's first tile
             for (int k = w.t0; k < w.t1; ++k) {
                 const int j0 = e.key_tile(k) * kKT;
                 const bool masked = masked_tile(a, e, j0);
                 const uint32_t fix = nFix;
                 nFix += masked;
-                if (!mine) continue;
-                if (ok) ok = mbar_wait(&barS[g], nS & 1, a.err);
+                if (pair && ((k - w.t0) & 1) != g) continue;
+                if (ok) ok = wait_on(&barS[g], nS & 1, a.err);
                 ++nS;
                 int dirty = 0;  // the stage of V (from 1) where this thread forms the product
                 if (masked && ok) {  // (after S: the tiles before this one have then been prepared)
-                    ok = mbar_wait(&barFix[fix % kFixDepth], (fix / kFixDepth) & 1, a.err);
+                    ok = wait_on(&barFix[fix % kFixDepth], (fix / kFixDepth) & 1, a.err);
                     dirty = max(dirty_sh[fix % kFixDepth][0], dirty_sh[fix % kFixDepth][1]);
                 }
                 if (!ok) break;
@@ -197,10 +245,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int j = 0; j < kKT; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+                    for (int j = 0; j < kKT; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], s[j], s[j + 1]);
                     const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                     const bool grow = mt > m + 8.0f;  // (from -infinity too; never for a row that sees nothing)
-                    if (k > w.t0 && __any_sync(kFull, grow && m != -INFINITY)) {
+                    if (k > kg && __any_sync(kFull, grow && m != -INFINITY)) {
                         const float f = grow ? tc::ex2(m - mt) : 1.0f;
                         l *= f;
 #pragma unroll 1
@@ -216,37 +264,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     }
                     if (grow) m = mt;
                     const float neg = m == -INFINITY ? 0.0f : -m;
-                    float ps[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float2 ps[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    const float2 scale = make_float2(sl2, sl2), shift = make_float2(neg, neg);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const float x0 = tc::ex2(fmaf(s[32 * c + 2 * j], sl2, neg)), x1 = tc::ex2(fmaf(s[32 * c + 2 * j + 1], sl2, neg));
-                            s[32 * c + 2 * j] = x0;
-                            s[32 * c + 2 * j + 1] = x1;
-                            ps[j & 3] += x0 + x1;
-                            pk[j] = pack_bf16(x0, x1);
+                            float2 x = fma2(make_float2(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), scale, shift);
+                            x.x = tc::ex2(x.x);
+                            x.y = tc::ex2(x.y);
+                            s[32 * c + 2 * j] = x.x;
+                            s[32 * c + 2 * j + 1] = x.y;
+                            ps[j & 1] = add2(ps[j & 1], x);
+                            pk[j] = pack_bf16(x.x, x.y);
                         }
                         if (!dirty) st16(tS + 16 * c, pk);
                     }
-                    l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                    ps[0] = add2(ps[0], ps[1]);
+                    l += ps[0].x + ps[0].y;
                     tc::wait_st();
                     if (dirty) {
-                        // P V by this row's thread: p in bf16 as the tensor cores take it (over S), V from the ring
+                        // P V by this row's thread: p over S (rounded to bf16 as the tensor cores take it), V from the ring
 #pragma unroll
-                        for (int c = 0; c < kKT; c += 32) {
-                            float p[32];
+                        for (int c = 0; c < kKT; c += 16) {
+                            uint32_t x[16];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) p[j] = __bfloat162float(__float2bfloat16_rn(s[c + j]));
-                            tc::st32(tS + c, p);
+                            for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(s[c + j]);
+                            st16(tS + c, x);
                         }
                         tc::wait_st();
                         const unsigned char* sV = sKV + (size_t)(dirty - 1) * C::kTile;
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             float o[32];
-                            if (k > w.t0) {
+                            if (k > kg) {
                                 tc::ld32(tO + c, o);
                                 tc::wait_ld();
                             } else {
@@ -255,8 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                             }
 #pragma unroll 1
                             for (int j = 0; j < kKT; ++j) {
-                                const float p = ld1(tS + j);
+                                float p = ld1(tS + j);
                                 tc::wait_ld();
+                                asm volatile("" : "+f"(p));
+                                p = __bfloat162float(__float2bfloat16_rn(p));
                                 const bool see = j <= hi && (j >= lo || j < sk);
                                 const unsigned char* vr = sV + (c >> 6) * kBox + j * 128;
 #pragma unroll
@@ -280,52 +334,87 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&barP[g]);
             }
-            if (!mine) continue;
-            if (ok) ok = mbar_wait(&barO[g], nO & 1, a.err);
-            ++nO;
+            const bool any = kg < w.t1;  // (a pair's second group may have no tile)
+            if (any) {
+                if (ok) ok = wait_on(&barO[g], nO & 1, a.err);
+                ++nO;
+            }
             if (!ok) break;
             tc::fence_after_sync();
             if (!warp_live) continue;
-            const size_t orow = (size_t)(e.row0 + g * TM + (live ? tok : 0)) * a.Hq + w.h * a.G + (live ? hrow : 0);
-            if (w.whole()) {
-                const bool empty = t < 0;
-                const float inv = empty ? 0.0f : 1.0f / l;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.O) + orow * D;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
+            // A pair's threads of one row are in warps of the same TMEM lanes: each joins half of the columns
+            // of both accumulators.
+            float f0 = 1.0f, f1 = 0.0f;  // factors of O_0 and O_1 (of O_g alone, if not a pair)
+            const bool both = pair && w.t1 - w.t0 > 1;
+            if (both) {
+                float2 x = make_float2(m, l), y = x;  // group 0's and group 1's, exchanged through one slot
+                if (g == 1) ml_sh[row] = y;
+                pair_sync(warp & 3);
+                if (g == 0) {
+                    y = ml_sh[row];
+                    ml_sh[row] = x;
+                }
+                pair_sync(warp & 3);
+                if (g == 1) x = ml_sh[row];
+                m = fmaxf(x.x, y.x);
+                // (a group of NaN scores alone has a sum and no maximum: NaN then)
+                f0 = x.x == -INFINITY && x.y == 0.0f ? 0.0f : tc::ex2(x.x - m);
+                f1 = y.x == -INFINITY && y.y == 0.0f ? 0.0f : tc::ex2(y.x - m);
+                l = x.y * f0 + y.y * f1;
+            }
+            const int c0 = both ? g * (D / 2) : 0, c1 = both ? c0 + D / 2 : D;
+            const bool writer = any && (!both || g == 0);  // of the row's maximum and sum
+            const size_t orow = (size_t)(e.row0 + tok0 + (live ? tok : 0)) * a.Hq + w.h * a.G + (live ? hrow : 0);
+            const bool whole = w.whole(), empty = t < 0;
+            float* rec = a.rec + (((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * (TQ * a.G) + (live ? (tok0 + tok) * a.G + hrow : 0)) * (D + 4);
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.O) + orow * D;
+            if (whole) {
+                f0 = empty ? 0.0f : f0 / l;
+                f1 = empty ? 0.0f : f1 / l;
+            }
+            if (any) {
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 32) {
                     float o[32];
-                    tc::ld32(tO + c, o);
+                    tc::ld32((both ? tmem + lanes + kColO : tO) + c, o);
                     tc::wait_ld();
-                    if (live) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = f0 != 0.0f ? o[j] * f0 : 0.0f;
+                    if (both) {
+                        float o1[32];
+                        tc::ld32(tmem + lanes + kColO + 128 + c, o1);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = f1 != 0.0f ? fmaf(o1[j], f1, o[j]) : o[j];
+                    }
+                    if (live && whole) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 8) {
                             uint4 v;
-                            v.x = pack_bf16(o[j] * inv, o[j + 1] * inv);
-                            v.y = pack_bf16(o[j + 2] * inv, o[j + 3] * inv);
-                            v.z = pack_bf16(o[j + 4] * inv, o[j + 5] * inv);
-                            v.w = pack_bf16(o[j + 6] * inv, o[j + 7] * inv);
-                            *reinterpret_cast<uint4*>(out + c + j) = empty ? make_uint4(0u, 0u, 0u, 0u) : v;
+                            v.x = pack_bf16(o[j], o[j + 1]);
+                            v.y = pack_bf16(o[j + 2], o[j + 3]);
+                            v.z = pack_bf16(o[j + 4], o[j + 5]);
+                            v.w = pack_bf16(o[j + 6], o[j + 7]);
+                            *reinterpret_cast<uint4*>(out + c + j) = v;
                         }
-                    }
-                }
-                if (live && a.lse) a.lse[orow] = empty ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-            } else {
-                float* rec = a.rec + (((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * (TQ * a.G) + (g * TM + tok) * a.G + hrow) * (D + 4);
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    tc::ld32(tO + c, o);
-                    tc::wait_ld();
-                    if (live) {
+                    } else if (live) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
                             *reinterpret_cast<float4*>(rec + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                 }
-                if (live) {
+            }
+            if (live && writer) {
+                if (whole) {
+                    if (a.lse) a.lse[orow] = empty ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                } else {
                     rec[D] = m;
                     rec[D + 1] = l;
                 }
+            }
+            if (both) {  // neither group's accumulator is written again before both have read it
+                tc::fence_before_sync();
+                pair_sync(warp & 3);
             }
         }
     } else {
@@ -360,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++n) {
                         const uint32_t s = n % C::kStages;
-                        if (n >= C::kStages && ok) ok = mbar_wait(&barFree[s], ((n / C::kStages) - 1) & 1, a.err);
+                        if (n >= C::kStages && ok) ok = wait_on(&barFree[s], ((n / C::kStages) - 1) & 1, a.err);
                         if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(&barKV[s], C::kTile);
                         __syncwarp();
@@ -372,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                         }
                     }
                     if (k == w.t0 && ok) {
-                        if (u > 0) ok = mbar_wait(&barQfree, (u - 1) & 1, a.err);
+                        if (u > 0) ok = wait_on(&barQfree, (u - 1) & 1, a.err);
                         if (ok && lane == 0) {
                             mbar_arrive_expect_tx(&barQ, (two ? 2 : 1) * C::H * a.G * TM * 128);
                             for (int g = 0; g < (two ? 2 : 1); ++g)
@@ -385,73 +474,95 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             }
             // wait for the copies that no one consumed (only after a wait that gave up)
             if (!ok)
-                for (uint32_t s = 0; s < C::kStages && s < n; ++s) mbar_wait(&barKV[s], ((n - 1 - s) / C::kStages) & 1, a.err);
+                for (uint32_t s = 0; s < C::kStages && s < n; ++s) wait_on(&barKV[s], ((n - 1 - s) / C::kStages) & 1, a.err);
         } else if (warp == kMmaWarp) {
-            // -------------------------------------------------------- tensor cores
-            const uint32_t q_addr = smem_addr(sQ), kv_addr = smem_addr(sKV);
-            uint32_t n = 0, u = 0, nFix = 0, nP[2] = {0, 0};
-            auto wait_stage = [&](uint32_t i) { if (ok) ok = mbar_wait(&barKV[i % C::kStages], (i / C::kStages) & 1, a.err); };
-            auto qk = [&](int g, uint32_t i) {
-                const uint32_t kb = kv_addr + (i % C::kStages) * C::kTile, qb = q_addr + g * C::kTile;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    tc::mma_f16_ss(tmem + 128 * g, tc::smem_desc_sw128(qb + (ks >> 2) * kBox + (ks & 3) * 32, 16, 1024),
-                                   tc::smem_desc_sw128(kb + (ks >> 2) * kBox + (ks & 3) * 32, 16, 1024), C::kIdescS, ks > 0);
-                tc::commit(&barS[g]);
-            };
-            for (; more && ok; more = w.next(a, TQ), ++u) {
-                const PagedEntry& e = w.e;
-                const int nb = e.n > TM ? 2 : 1;
-                if (ok) ok = mbar_wait(&barQ, u & 1, a.err);
-                wait_stage(n);
-                if (!ok) break;
-                tc::fence_after_sync();
-                if (lane == 0) {
-                    for (int g = 0; g < nb; ++g) qk(g, n);
-                    tc::commit(&barFree[n % C::kStages]);
-                    if (w.t1 - w.t0 == 1) tc::commit(&barQfree);
-                }
-                for (int k = w.t0; k < w.t1 && ok; ++k, n += 2) {
-                    const bool last = k + 1 == w.t1;
-                    bool dirty = false;
-                    if (!last) wait_stage(n + 2);
-                    wait_stage(n + 1);
-                    if (masked_tile(a, e, e.key_tile(k) * kKT)) {
-                        if (ok) ok = mbar_wait(&barFix[nFix % kFixDepth], (nFix / kFixDepth) & 1, a.err);
-                        dirty = (dirty_sh[nFix % kFixDepth][0] | dirty_sh[nFix % kFixDepth][1]) != 0;
-                        ++nFix;
+            // -------------------------------------------------------- tensor cores (one thread)
+            if (lane == 0) {
+                const uint64_t desc = tc::smem_desc_sw128(0, 16, 1024), desc_v = tc::smem_desc_sw128(0, kBox, 1024);
+                const uint64_t q_desc = desc + (smem_addr(sQ) >> 4), kv_addr = smem_addr(sKV) >> 4;
+                uint32_t u = 0, nFix = 0, nP[2] = {0, 0};
+                // positions in the ring: stage and phase of the tile's K (V follows), without divisions
+                struct Pos {
+                    uint32_t s, ph;
+                    __device__ __forceinline__ Pos plus(uint32_t k) const {
+                        const uint32_t t = s + k;
+                        return t >= C::kStages ? Pos{t - C::kStages, ph ^ 1u} : Pos{t, ph};
                     }
-                    const uint32_t vb = kv_addr + ((n + 1) % C::kStages) * C::kTile;
-                    for (int g = 0; g < nb && ok; ++g) {
-                        ok = mbar_wait(&barP[g], nP[g] & 1, a.err);
-                        ++nP[g];
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        if (lane == 0) {
-                            if (!dirty) {
+                };
+                Pos n{0, 0};
+                auto wait_stage = [&](Pos i) { if (ok) ok = wait_on(&barKV[i.s], i.ph, a.err); };
+                auto free_stage = [&](Pos i) { tc::commit(&barFree[i.s]); };
+                // S_g = Q_q K^T with K at position i of the ring
+                auto qk = [&](int g, int q, Pos i) {
+                    const uint64_t kb = desc + kv_addr + i.s * (C::kTile >> 4), qb = q_desc + q * (C::kTile >> 4);
 #pragma unroll
-                                for (int kk = 0; kk < kKT / 16; ++kk)
-                                    mma_f16_ts(tmem + kColO + 128 * g, tmem + 128 * g + 8 * kk,
-                                               tc::smem_desc_sw128(vb + kk * 16 * 128, kBox, 1024), C::kIdescPV, k > w.t0 || kk > 0);
-                            }
-                            if (g == nb - 1) tc::commit(&barFree[(n + 1) % C::kStages]);
-                            if (last) {
-                                tc::commit(&barO[g]);
-                            } else {
-                                qk(g, n + 2);
-                                if (g == nb - 1) {
-                                    tc::commit(&barFree[(n + 2) % C::kStages]);
-                                    if (k + 2 == w.t1) tc::commit(&barQfree);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint64_t at = ((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
+                        tc::mma_f16_ss(tmem + 128 * g, qb + at, kb + at, C::kIdescS, ks > 0);
+                    }
+                    tc::commit(&barS[g]);
+                };
+                // O_g (+)= P_g V with V at position i
+                auto pv = [&](int g, Pos i, bool add) {
+                    const uint64_t vb = desc_v + kv_addr + i.s * (C::kTile >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kKT / 16; ++kk)
+                        mma_f16_ts(tmem + kColO + 128 * g, tmem + 128 * g + 8 * kk, vb + kk * (16 * 128 >> 4), C::kIdescPV, add || kk > 0);
+                };
+                for (; more && ok; more = w.next(a, TQ), ++u) {
+                    const PagedEntry& e = w.e;
+                    const bool pair = e.n <= TM;
+                    const int nt = w.t1 - w.t0, ahead = pair ? 2 : 1;  // a group's next tile
+                    if (ok) ok = wait_on(&barQ, u & 1, a.err);
+                    wait_stage(n);
+                    if (pair && nt > 1) wait_stage(n.plus(2));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    qk(0, 0, n);
+                    if (pair) {
+                        free_stage(n);
+                        if (nt > 1) {
+                            qk(1, 0, n.plus(2));
+                            free_stage(n.plus(2));
+                        }
+                    } else {
+                        qk(1, 1, n);
+                        free_stage(n);
+                    }
+                    if (nt <= ahead) tc::commit(&barQfree);
+                    for (int k = 0; k < nt && ok; ++k, n = n.plus(2)) {
+                        const bool more_tiles = k + ahead < nt;
+                        const Pos v = n.plus(1), kn = n.plus(2 * ahead);
+                        bool dirty = false;
+                        wait_stage(v);
+                        if (more_tiles) wait_stage(kn);
+                        if (masked_tile(a, e, e.key_tile(w.t0 + k) * kKT)) {
+                            if (ok) ok = wait_on(&barFix[nFix % kFixDepth], (nFix / kFixDepth) & 1, a.err);
+                            dirty = (dirty_sh[nFix % kFixDepth][0] | dirty_sh[nFix % kFixDepth][1]) != 0;
+                            ++nFix;
+                        }
+                        const int ga = pair ? k & 1 : 0, gb = pair ? ga : 1;
+                        for (int g = ga; g <= gb && ok; ++g) {
+                            ok = wait_on(&barP[g], nP[g] & 1, a.err);
+                            ++nP[g];
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            if (!dirty) pv(g, v, k >= ahead);
+                            if (g == gb) free_stage(v);
+                            if (more_tiles) {
+                                qk(g, pair ? 0 : g, kn);
+                                if (g == gb) {
+                                    free_stage(kn);
+                                    if (k + ahead + 1 == nt) tc::commit(&barQfree);  // the unit's last use of Q
                                 }
+                            } else {
+                                tc::commit(&barO[g]);
                             }
                         }
-                        __syncwarp();
                     }
                 }
-            }
-            if (lane == 0) {  // the issuing thread stays until its MMAs are done
-                tc::commit(&barDone);
-                mbar_wait(&barDone, 0, a.err);
+                tc::commit(&barDone);  // the issuing thread stays until its MMAs are done
+                wait_on(&barDone, 0, a.err);
             }
         } else {
             // -------------------------------------------------------- V of the masked tiles
@@ -465,27 +576,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 for (int k = w.t0; k < w.t1 && ok; ++k, n += 2) {
                     const int j0 = e.key_tile(k) * kKT;
                     const uint32_t sk = n % C::kStages, s = (n + 1) % C::kStages;
-                    ok = mbar_wait(&barKV[sk], (n / C::kStages) & 1, a.err);
+                    ok = wait_on(&barKV[sk], (n / C::kStages) & 1, a.err);
                     if (ok && lane == 0) mbar_arrive(&barFree[sk]);
-                    if (ok) ok = mbar_wait(&barKV[s], ((n + 1) / C::kStages) & 1, a.err);
+                    if (ok) ok = wait_on(&barKV[s], ((n + 1) / C::kStages) & 1, a.err);
                     if (!ok) break;
                     if (masked_tile(a, e, j0)) {
                         unsigned char* sV = sKV + (size_t)s * C::kTile;
-                        bool odd = false;
-#pragma unroll 4
+                        const bool look = e.n > 1;  // (a single token's rows see the same keys)
+                        uint32_t inf = 0;           // exponents of all ones carry into the sign bits
+#pragma unroll 8
                         for (int c = f; c < C::H * 128 * 8; c += 64) {
                             const int j = j0 + ((c >> 3) & 127);
                             uint4* at = reinterpret_cast<uint4*>(sV + (size_t)c * 16);
-                            if (j <= hi && (j >= e.lo || j < a.S)) {
-                                const uint4 v = *at;
-                                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    odd |= (x[y] & 0x7f80u) == 0x7f80u || (x[y] & 0x7f800000u) == 0x7f800000u;
-                            } else {
+                            if (!(j <= hi && (j >= e.lo || j < a.S))) {
                                 *at = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (look) {
+                                const uint4 v = *at;
+                                inf |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                                       ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
                             }
                         }
+                        bool odd = (inf & 0x80008000u) != 0;
                         fence_proxy_async();
                         odd = __any_sync(kFull, odd);
                         __syncwarp();

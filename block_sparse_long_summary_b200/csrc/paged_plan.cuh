@@ -231,13 +231,15 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int r, int slot, bool
 }
 
 // Joins the records of every unit that range boundaries cut. Block (c, y): boundary c (the start of
-// worker c's range) if it is the first one inside its unit; the unit's rows y, y + gridDim.y, ...,
-// one warp each. Records lie in the order of the workers, so the sum's order is fixed.
+// worker c's range) if it is the first one inside its unit; the unit's rows 4 y + warp, then every
+// 4 gridDim.y, one warp each. Lane i looks after piece i (32 at a time): the pieces' tile counts,
+// maxima and sums come in one round trip each, then the outputs without waiting on one another.
+// Pieces lie in the order of the workers, so the order of the sums is fixed.
 template <typename T, int D, int KT>
 __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int TQ, int n_workers, int rec_rows) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x + 1;
-    const int4 s = a.seg[c];
+    const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 s = a.seg[c], before = a.seg[c - 1];
     if (s.w == 0) return;
     int row_r, n_r, L_r;
     bool bad;
@@ -245,42 +247,70 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int TQ, i
     const PagedEntry e = make_entry<KT>(a, s.x, s.y, TQ, row_r, n_r, L_r);
     const int h = s.z / e.nt, t0 = s.z - h * e.nt;
     if (t0 == 0) return;
-    // the worker before: is this boundary the first one inside the unit?
+    // the last worker before with tiles (some have none where there are fewer tiles than workers)
     int p = c - 1;
-    while (p > 0 && a.seg[p].w == 0) --p;  // workers without tiles (fewer tiles than workers)
-    const int4 q = a.seg[p];
+    int4 q = before;
+    while (p > 0 && q.w == 0) q = a.seg[--p];
     const bool same = q.x == s.x && q.y == s.y && q.z / e.nt == h;
-    if (same && q.z - h * e.nt > 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (same && q.z - h * e.nt > 0) return;  // an earlier boundary inside this unit
     constexpr int C = D / 32;
     for (int row = blockIdx.y * 4 + warp; row < e.n * a.G; row += gridDim.y * 4) {
         float M = -INFINITY, l = 0.0f, o[C];
 #pragma unroll
         for (int k = 0; k < C; ++k) o[k] = 0.0f;
-        int w = p, slot = same ? 0 : 1;
-        int end = t0;  // tiles covered so far
-        while (true) {
-            const float* rec = a.rec + (((size_t)w * 2 + slot) * rec_rows + row) * (D + 4);
-            const float m1 = rec[D], l1 = rec[D + 1];
-            if (m1 != -INFINITY || l1 != 0.0f) {  // (a piece of NaN scores alone has a sum and no maximum)
-                const float nm = fmaxf(M, m1);
-                const float f0 = M == -INFINITY ? 0.0f : exp2f(M - nm), f1 = exp2f(m1 - nm);
-                l = l * f0 + l1 * f1;
+        int covered = t0;      // tiles of the unit in the pieces up to worker w0 - 1 (the first one's end at t0)
+        for (int w0 = p; w0 < n_workers; w0 += 32) {
+            const int w = w0 + lane;
+            const int tiles = w > p && w < n_workers ? a.seg[w].w : 0;
+            int inc = tiles;
 #pragma unroll
-                for (int k = 0; k < C; ++k) o[k] = o[k] * f0 + rec[lane * C + k] * f1;
-                M = nm;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(kFull, inc, d);
+                if (lane >= d) inc += u;
             }
-            if (end >= e.nt) break;
-            ++w;
-            while (w < n_workers && a.seg[w].w == 0) ++w;
-            if (w >= n_workers) break;
-            slot = 0;
-            end += a.seg[w].w;
+            // a piece: the first worker, and those whose range begins before the unit's end
+            const bool piece = w == p || (tiles > 0 && covered + inc - tiles < e.nt);
+            const float* rec = a.rec + (((size_t)w * 2 + (w == p && !same ? 1 : 0)) * rec_rows + row) * (D + 4);
+            const float m1 = piece ? rec[D] : -INFINITY, l1 = piece ? rec[D + 1] : 0.0f;
+            float nm = m1;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(kFull, nm, d));
+            nm = fmaxf(nm, M);
+            const float f0 = M == -INFINITY ? 0.0f : exp2f(M - nm);
+            // (a piece of NaN scores alone has a sum and no maximum: NaN then)
+            const float f1 = m1 == -INFINITY && l1 == 0.0f ? 0.0f : exp2f(m1 - nm);
+            float sum = l1 * f1;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+            l = l * f0 + sum;
+#pragma unroll
+            for (int k = 0; k < C; ++k) o[k] *= f0;
+            M = nm;
+            const unsigned who = __ballot_sync(kFull, piece && f1 != 0.0f);  // (NaN counts)
+            const int first = __ffs(who) - 1, last = 31 - __clz(who);
+            if (who) {
+#pragma unroll 8
+                for (int i = first; i <= last; ++i) {
+                    const float f = __shfl_sync(kFull, f1, i);
+                    if (!(who >> i & 1u)) continue;
+                    const float* src = a.rec + (((size_t)(w0 + i) * 2 + (w0 + i == p && !same ? 1 : 0)) * rec_rows + row) * (D + 4) + lane * C;
+                    float v[C];
+                    if constexpr (C == 4) {
+                        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+                    } else {
+                        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+                    }
+#pragma unroll
+                    for (int k = 0; k < C; ++k) o[k] = fmaf(v[k], f, o[k]);
+                }
+            }
+            covered += __shfl_sync(kFull, inc, 31);
+            if (covered >= e.nt) break;
         }
         const int tok = row / a.G;
         const size_t orow = (size_t)(e.row0 + tok) * a.Hq + h * a.G + row % a.G;
         const bool empty = e.pos0 + tok < 0;
-        const float inv = empty ? 0.0f : 1.0f / l;
+        const float inv = 1.0f / l;
 #pragma unroll
         for (int k = 0; k < C; ++k)
             Elem<T>::store(static_cast<T*>(a.O) + orow * D + lane * C + k, empty ? 0.0f : o[k] * inv);
