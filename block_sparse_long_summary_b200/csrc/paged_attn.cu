@@ -20,15 +20,15 @@ Layout layout_of(const PagedDims& m) {
     const bool tensor = m.dtype == COBS_BF16;
     l.workers = tensor ? paged_chunk_workers(m) : paged_simt_workers(m);
     l.rec_rows = tensor ? paged_chunk_rec_rows(m) : paged_simt_rec_rows(m);
-    l.seg_bytes = al256((size_t)l.workers * sizeof(int4));
-    l.rec_bytes = (size_t)l.workers * 2 * l.rec_rows * (m.d + 4) * sizeof(float);
+    l.seg_bytes = al256((size_t)l.workers * sizeof(PagedSeg));
+    l.rec_bytes = (size_t)l.workers * 2 * l.rec_rows * (m.d + 2) * sizeof(float);
     return l;
 }
 
 }  // namespace
 
 // [workers] ranges, then two records per worker (the first and the last unit of its range may be
-// pieces): rec_rows x (d + 4) float32.
+// pieces): rec_rows x (d + 2) float32.
 size_t paged_attn_workspace_bytes(const PagedDims& m) {
     const Layout l = layout_of(m);
     return l.seg_bytes + l.rec_bytes;
@@ -40,7 +40,8 @@ cudaError_t launch_paged_attn(const PagedDims& m, const void* Q, const void* k_c
     const Layout l = layout_of(m);
     PagedArgs a{};
     a.table = block_table; a.cu = cu_new; a.kv_len = kv_len; a.lse = lse; a.O = O; a.err = err;
-    a.seg = static_cast<int4*>(ws);
+    a.seg = static_cast<PagedSeg*>(ws);
+    a.rec_rows = l.rec_rows;
     a.rec = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + l.seg_bytes);
     a.R = m.R; a.Hq = m.Hq; a.Hkv = m.Hkv; a.G = m.G; a.page = m.page; a.page_shift = m.page_shift;
     a.n_pages = m.n_pages; a.max_pages = m.max_pages; a.n_tokens = m.n_tokens; a.max_new = m.max_new;

@@ -19,7 +19,7 @@
 // each with an accumulator and maxima of its own, joined at the unit's end.
 // Roles: warps 0-3 and 4-7 softmax and epilogue of row tiles 0 and 1; warp 8 loads (one TMA box per
 // page and 64 columns; pages no row needs come as out-of-range boxes, that is zeros); warp 9 issues
-// the MMAs; warps 10 and 11 prepare V of the tiles that some row does not see in full: rows of V no
+// the MMAs; warps 10 and 11 (the first also loads Q) prepare V of the tiles that some row does not see in full: rows of V no
 // row of the unit sees (slots behind the keys, keys before the window: any bits) are set to zero,
 // since 0 * NaN would reach O, and the others are looked over for infinities and NaN: such a tile's
 // product is formed by the softmax threads, key by key, so that only the rows that see them change.
@@ -94,6 +94,11 @@ __device__ __forceinline__ float ld1(uint32_t taddr) {
 }
 // The two warps (one of each group) that hold the same rows.
 __device__ __forceinline__ void pair_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory"); }
+template <int N> __device__ __forceinline__ void rows_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
+// shared memory to global, both 16-byte aligned, a multiple of 16 bytes
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
+}
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -118,6 +123,8 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err
     return false;
 }
 
+// n ones from bit 0 up (none for n <= 0, all for n >= 32)
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -138,6 +145,37 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     return r;
 }
 
+// A position in the ring: stage, and parity of its phase.
+template <int STAGES>
+struct Pos {
+    uint32_t s = 0, ph = 0;
+    __device__ __forceinline__ Pos plus(uint32_t k) const {  // k <= STAGES
+        const uint32_t t = s + k;
+        return t >= STAGES ? Pos{t - STAGES, ph ^ 1u} : Pos{t, ph};
+    }
+    __device__ __forceinline__ void advance(uint32_t k) {
+        const uint32_t t = s + k, q = t / STAGES;
+        s = t - q * STAGES;
+        ph ^= q & 1u;
+    }
+};
+
+// How a unit runs: one row tile whose key tiles the two groups take in turn, or two; and whether its
+// output leaves through the ring (a stage per row tile, rows written to shared memory and copied out in
+// bulk): a thread's row is 2 d bytes apart from its neighbour's, so direct stores of 32 rows touch 32
+// lines each, which took 7k cycles per unit of 256 rows against 1k through the ring. One warp's rows and
+// records go directly.
+template <int KT>
+struct Shape {
+    bool pair, staged;
+    uint32_t stages;  // of the output
+    __device__ __forceinline__ Shape(const PagedArgs& a, const PagedWalk<KT>& w, int TM) {
+        pair = w.e.n <= TM;
+        staged = w.whole() && w.e.n * a.G > 32;
+        stages = staged ? (pair ? 1 : 2) : 0;
+    }
+};
+
 struct ChunkMaps {
     CUtensorMap q, k, v;
 };
@@ -154,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     __shared__ __align__(8) uint64_t barQ, barQfree, barKV[C::kStages], barFree[C::kStages], barS[2], barP[2], barO[2], barFix[kFixDepth], barDone;
     __shared__ uint32_t tmem_sh;
     __shared__ int dirty_sh[kFixDepth][2];
-    __shared__ long long tmp[kThreads / 32];
+    __shared__ long long tmp[2 * kThreads / 32];
     __shared__ PagedRange range;
     __shared__ float2 ml_sh[128];  // a pair's maxima and sums
     unsigned char* sQ = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -182,8 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         mbar_init(&barDone, 1);
         fence_barrier_init();
     }
-    plan_ranges<kThreads, kKT, 1>(a, TQ, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sKV), tmp, &range);
-    if (tid == 0) a.seg[blockIdx.x] = make_int4(range.r, range.i, range.off, range.count);
+    plan_range<kThreads, kKT>(a, TQ, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sKV), tmp, &range);
     fence_proxy_async();  // the plan's use of the ring before TMA's
     tc::fence_before_sync();
     __syncthreads();
@@ -193,9 +230,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     bool ok = true;
     PagedWalk<kKT> w;
     bool more = w.first(a, TQ, rg);
+    if (tid == kFixWarp * 32) a.seg[blockIdx.x] = w.seg(rg);
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax and epilogue of row tile g
+        // (after a wait that gave up these warps go on without waiting: they meet at named barriers)
         reg_inc<216>();
         const int g = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -203,10 +242,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         const int tok = row / a.G, hrow = row - tok * a.G;
         const float sl2 = a.sl2;
         uint32_t nS = 0, nO = 0, nFix = 0;
+        Pos<C::kStages> at;  // of the unit's first tile
         int piece = 0;
-        for (; more && ok; more = w.next(a, TQ), ++piece) {
+        for (; more; more = w.next(a, TQ), ++piece) {
             const PagedEntry& e = w.e;
-            const bool pair = e.n <= TM;              // one row tile: the groups take its key tiles in turn
+            const Shape<kKT> sh(a, w, TM);
+            const bool pair = sh.pair;
             const int tok0 = pair ? 0 : g * TM;       // first token of this group's rows
             const int ntok = min(TM, e.n - tok0);
             const bool live = tok < ntok;
@@ -227,7 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     ok = wait_on(&barFix[fix % kFixDepth], (fix / kFixDepth) & 1, a.err);
                     dirty = max(dirty_sh[fix % kFixDepth][0], dirty_sh[fix % kFixDepth][1]);
                 }
-                if (!ok) break;
                 tc::fence_after_sync();
                 if (warp_live) {
                     float s[kKT];
@@ -241,7 +281,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     const int hi = t - j0, lo = a.W > 0 ? hi - a.W + 1 : 0, sk = a.W > 0 ? a.S - j0 : 0;
                     if (masked) {
 #pragma unroll
-                        for (int j = 0; j < kKT; ++j) s[j] = (j <= hi && (j >= lo || j < sk)) ? s[j] : -INFINITY;
+                        for (int c = 0; c < kKT; c += 32) {
+                            const uint32_t see = bits_below(hi - c + 1) & (~bits_below(lo - c) | bits_below(sk - c));
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) s[c + j] = see & (1u << j) ? s[c + j] : -INFINITY;
+                        }
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -274,8 +318,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                             float2 x = fma2(make_float2(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), scale, shift);
                             x.x = tc::ex2(x.x);
                             x.y = tc::ex2(x.y);
-                            s[32 * c + 2 * j] = x.x;
-                            s[32 * c + 2 * j + 1] = x.y;
                             ps[j & 1] = add2(ps[j & 1], x);
                             pk[j] = pack_bf16(x.x, x.y);
                         }
@@ -285,15 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     l += ps[0].x + ps[0].y;
                     tc::wait_st();
                     if (dirty) {
-                        // P V by this row's thread: p over S (rounded to bf16 as the tensor cores take it), V from the ring
-#pragma unroll
-                        for (int c = 0; c < kKT; c += 16) {
-                            uint32_t x[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(s[c + j]);
-                            st16(tS + c, x);
-                        }
-                        tc::wait_st();
+                        // P V by this row's thread: p again from S (P has not replaced it), rounded to bf16 as the
+                        // tensor cores take it, V from the ring
                         const unsigned char* sV = sKV + (size_t)(dirty - 1) * C::kTile;
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
@@ -310,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                                 float p = ld1(tS + j);
                                 tc::wait_ld();
                                 asm volatile("" : "+f"(p));
-                                p = __bfloat162float(__float2bfloat16_rn(p));
+                                p = __bfloat162float(__float2bfloat16_rn(tc::ex2(fmaf(p, sl2, neg))));
                                 const bool see = j <= hi && (j >= lo || j < sk);
                                 const unsigned char* vr = sV + (c >> 6) * kBox + j * 128;
 #pragma unroll
@@ -339,137 +374,160 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 if (ok) ok = wait_on(&barO[g], nO & 1, a.err);
                 ++nO;
             }
-            if (!ok) break;
+            at.advance(2 * (w.t1 - w.t0));  // the output's first stage
+            const Pos<C::kStages> mine = at.plus(pair ? 0 : g);
+            at.advance(sh.stages);
+            if (ok && sh.staged) ok = wait_on(&barKV[mine.s], mine.ph, a.err);
             tc::fence_after_sync();
-            if (!warp_live) continue;
             // A pair's threads of one row are in warps of the same TMEM lanes: each joins half of the columns
             // of both accumulators.
             float f0 = 1.0f, f1 = 0.0f;  // factors of O_0 and O_1 (of O_g alone, if not a pair)
-            const bool both = pair && w.t1 - w.t0 > 1;
-            if (both) {
-                float2 x = make_float2(m, l), y = x;  // group 0's and group 1's, exchanged through one slot
-                if (g == 1) ml_sh[row] = y;
-                pair_sync(warp & 3);
-                if (g == 0) {
-                    y = ml_sh[row];
-                    ml_sh[row] = x;
+            const bool both = pair && w.t1 - w.t0 > 1, empty = t < 0, whole = w.whole();
+            if (warp_live) {
+                if (both) {
+                    float2 x = make_float2(m, l), y = x;  // group 0's and group 1's, exchanged through one slot
+                    if (g == 1) ml_sh[row] = y;
+                    pair_sync(warp & 3);
+                    if (g == 0) {
+                        y = ml_sh[row];
+                        ml_sh[row] = x;
+                    }
+                    pair_sync(warp & 3);
+                    if (g == 1) x = ml_sh[row];
+                    m = fmaxf(x.x, y.x);
+                    // (a group of NaN scores alone has a sum and no maximum: NaN then)
+                    f0 = x.x == -INFINITY && x.y == 0.0f ? 0.0f : tc::ex2(x.x - m);
+                    f1 = y.x == -INFINITY && y.y == 0.0f ? 0.0f : tc::ex2(y.x - m);
+                    l = x.y * f0 + y.y * f1;
                 }
-                pair_sync(warp & 3);
-                if (g == 1) x = ml_sh[row];
-                m = fmaxf(x.x, y.x);
-                // (a group of NaN scores alone has a sum and no maximum: NaN then)
-                f0 = x.x == -INFINITY && x.y == 0.0f ? 0.0f : tc::ex2(x.x - m);
-                f1 = y.x == -INFINITY && y.y == 0.0f ? 0.0f : tc::ex2(y.x - m);
-                l = x.y * f0 + y.y * f1;
-            }
-            const int c0 = both ? g * (D / 2) : 0, c1 = both ? c0 + D / 2 : D;
-            const bool writer = any && (!both || g == 0);  // of the row's maximum and sum
-            const size_t orow = (size_t)(e.row0 + tok0 + (live ? tok : 0)) * a.Hq + w.h * a.G + (live ? hrow : 0);
-            const bool whole = w.whole(), empty = t < 0;
-            float* rec = a.rec + (((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * (TQ * a.G) + (live ? (tok0 + tok) * a.G + hrow : 0)) * (D + 4);
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.O) + orow * D;
-            if (whole) {
-                f0 = empty ? 0.0f : f0 / l;
-                f1 = empty ? 0.0f : f1 / l;
-            }
-            if (any) {
+                const int c0 = both ? g * (D / 2) : 0, c1 = both ? c0 + D / 2 : D;
+                const size_t orow = (size_t)(e.row0 + tok0 + (live ? tok : 0)) * a.Hq + w.h * a.G + (live ? hrow : 0);
+                float* rec = a.rec + ((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * a.rec_rows * (D + 2);
+                const int rrow = live ? (tok0 + tok) * a.G + hrow : 0;
+                unsigned char* out = sh.staged ? sKV + (size_t)mine.s * C::kTile + row * (2 * D)
+                                               : reinterpret_cast<unsigned char*>(static_cast<__nv_bfloat16*>(a.O) + orow * D);
+                if (whole) {
+                    f0 = empty ? 0.0f : f0 / l;
+                    f1 = empty ? 0.0f : f1 / l;
+                }
+                if (any) {
 #pragma unroll 1
-                for (int c = c0; c < c1; c += 32) {
-                    float o[32];
-                    tc::ld32((both ? tmem + lanes + kColO : tO) + c, o);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = f0 != 0.0f ? o[j] * f0 : 0.0f;
-                    if (both) {
-                        float o1[32];
-                        tc::ld32(tmem + lanes + kColO + 128 + c, o1);
+                    for (int c = c0; c < c1; c += 32) {
+                        float o[32];
+                        tc::ld32((both ? tmem + lanes + kColO : tO) + c, o);
                         tc::wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = f1 != 0.0f ? fmaf(o1[j], f1, o[j]) : o[j];
-                    }
-                    if (live && whole) {
+                        for (int j = 0; j < 32; ++j) o[j] = f0 != 0.0f ? o[j] * f0 : 0.0f;
+                        if (both) {
+                            float o1[32];
+                            tc::ld32(tmem + lanes + kColO + 128 + c, o1);
+                            tc::wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint4 v;
-                            v.x = pack_bf16(o[j], o[j + 1]);
-                            v.y = pack_bf16(o[j + 2], o[j + 3]);
-                            v.z = pack_bf16(o[j + 4], o[j + 5]);
-                            v.w = pack_bf16(o[j + 6], o[j + 7]);
-                            *reinterpret_cast<uint4*>(out + c + j) = v;
+                            for (int j = 0; j < 32; ++j) o[j] = f1 != 0.0f ? fmaf(o1[j], f1, o[j]) : o[j];
                         }
-                    } else if (live) {
+                        if (whole) {
+                            uint4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4*>(rec + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                            for (int j = 0; j < 4; ++j)
+                                v[j] = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
+                                                  pack_bf16(o[8 * j + 4], o[8 * j + 5]), pack_bf16(o[8 * j + 6], o[8 * j + 7]));
+                            if (sh.staged) {
+                                // the rows' common pitch puts a chunk of all rows in the same banks: lane r
+                                // writes chunk (j + r) % 4 in step j, two steps of exchange
+                                const bool r1 = lane & 1, r2 = lane & 2;
+                                const uint4 w0 = r1 ? v[1] : v[0], w1 = r1 ? v[2] : v[1], w2 = r1 ? v[3] : v[2], w3 = r1 ? v[0] : v[3];
+                                v[0] = r2 ? w2 : w0;
+                                v[1] = r2 ? w3 : w1;
+                                v[2] = r2 ? w0 : w2;
+                                v[3] = r2 ? w1 : w3;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(out + 2 * c + 16 * ((j + lane) & 3)) = v[j];
+                            } else if (live) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(out + 2 * c + 16 * j) = v[j];
+                            }
+                        } else if (live) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                reinterpret_cast<float4*>(rec)[(size_t)((c + j) >> 2) * a.rec_rows + rrow] =
+                                    make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
+                    }
+                }
+                if (live && any && (!both || g == 0)) {
+                    if (!whole) {
+                        reinterpret_cast<float2*>(rec + (size_t)a.rec_rows * D)[rrow] = make_float2(m, l);
+                    } else if (a.lse) {
+                        a.lse[orow] = empty ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                     }
                 }
             }
-            if (live && writer) {
-                if (whole) {
-                    if (a.lse) a.lse[orow] = empty ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-                } else {
-                    rec[D] = m;
-                    rec[D + 1] = l;
+            // neither group's accumulator is written again before both have read it
+            tc::fence_before_sync();
+            if (sh.staged) {
+                fence_proxy_async();
+                if (pair) rows_sync<256>(5); else rows_sync<128>(5 + g);
+                if ((warp & 3) == 0 && (!pair || g == 0)) {  // a token's rows of the group are one run of both memories
+                    const unsigned char* src = sKV + (size_t)mine.s * C::kTile;
+                    for (int i = lane; i < ntok; i += 32)
+                        bulk_s2g(static_cast<__nv_bfloat16*>(a.O) + ((size_t)(e.row0 + tok0 + i) * a.Hq + w.h * a.G) * D,
+                                 src + (size_t)i * a.G * 2 * D, a.G * 2 * D);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&barFree[mine.s]);
                 }
-            }
-            if (both) {  // neither group's accumulator is written again before both have read it
-                tc::fence_before_sync();
+            } else if (both && warp_live) {
                 pair_sync(warp & 3);
             }
         }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
         reg_dec<72>();
         if (warp == kLoadWarp) {
             // -------------------------------------------------------- loads
-            const int ppt = kKT >> a.page_shift, per = 32 / ppt;  // pages per tile, tiles per look-up of 32 entries
+            const int shift = 7 - a.page_shift, ppt = 1 << shift, per = 32 >> shift;  // pages per tile, tiles per look-up
+            const int my_tile = lane >> shift, my_key = (lane & (ppt - 1)) << a.page_shift;
             const uint32_t zero_box = (uint32_t)a.n_pages * a.Hkv;
-            uint32_t n = 0, u = 0;
-            for (; more && ok; more = w.next(a, TQ), ++u) {
+            uint32_t n = 0;
+            Pos<C::kStages> at;
+            for (; more && ok; more = w.next(a, TQ)) {
                 const PagedEntry& e = w.e;
                 const int hi = e.last_pos();
-                const bool two = e.n > TM;
-                auto first_key = [&](int k0) { return k0 + lane / ppt < w.t1 ? (e.key_tile(k0 + lane / ppt) * kKT + ((lane % ppt) << a.page_shift)) : -1; };
-                auto entry = [&](int k0) {  // raw table entry of this lane's page
-                    const int j = first_key(k0), slot = j >> a.page_shift;
-                    return j >= 0 && j <= hi && slot < a.max_pages && (j + a.page > e.lo || j < a.S)
-                               ? __ldg(a.table + (size_t)e.r * a.max_pages + slot) : INT_MIN;
+                auto entry = [&](int k) {  // raw table entry of this lane's page of the look-up from tile k
+                    const int j = k + my_tile < w.t1 ? e.key_tile(k + my_tile) * kKT + my_key : INT_MAX;
+                    return j <= hi && (j >> a.page_shift) < a.max_pages && (j + a.page > e.lo || j < a.S)
+                               ? __ldg(a.table + (size_t)e.r * a.max_pages + (j >> a.page_shift)) : INT_MIN;
                 };
                 int raw = entry(w.t0), k0 = w.t0;
                 uint32_t z = 0;
                 for (int k = w.t0; k < w.t1 && ok; ++k) {
                     if (k == w.t0 || k == k0 + per) {
-                        if (k != w.t0) k0 = k;
+                        k0 = k;
                         // pages no row needs, and (recorded) those outside the cache, read as zeros
                         const bool in = raw >= 0 && raw < a.n_pages;
                         if (!in && raw != INT_MIN) report_error(a.err, kErrBadIndex);
                         z = in ? (uint32_t)raw * a.Hkv + w.h : zero_box;
                         raw = entry(k0 + per);
                     }
-                    const uint32_t zt = __shfl_sync(kFull, z, (k - k0) * ppt + (lane & (ppt - 1)));
+                    const uint32_t zt = __shfl_sync(kFull, z, ((k - k0) << shift) + (lane & (ppt - 1)));
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++n) {
-                        const uint32_t s = n % C::kStages;
-                        if (n >= C::kStages && ok) ok = wait_on(&barFree[s], ((n / C::kStages) - 1) & 1, a.err);
+                    for (int kv = 0; kv < 2; ++kv, ++n, at = at.plus(1)) {
+                        if (ok) ok = wait_on(&barFree[at.s], at.ph ^ 1, a.err);
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&barKV[s], C::kTile);
+                        if (lane == 0) mbar_arrive_expect_tx(&barKV[at.s], C::kTile);
                         __syncwarp();
                         if (lane < ppt) {
-                            unsigned char* dst = sKV + (size_t)s * C::kTile + (lane << a.page_shift) * 128;
+                            unsigned char* dst = sKV + (size_t)at.s * C::kTile + my_key * 128;
 #pragma unroll
                             for (int h = 0; h < C::H; ++h)
-                                tma_load_3d(dst + h * kBox, kv == 0 ? &maps.k : &maps.v, 64 * h, 0, (int)zt, &barKV[s]);
+                                tma_load_3d(dst + h * kBox, kv == 0 ? &maps.k : &maps.v, 64 * h, 0, (int)zt, &barKV[at.s]);
                         }
                     }
-                    if (k == w.t0 && ok) {
-                        if (u > 0) ok = wait_on(&barQfree, (u - 1) & 1, a.err);
-                        if (ok && lane == 0) {
-                            mbar_arrive_expect_tx(&barQ, (two ? 2 : 1) * C::H * a.G * TM * 128);
-                            for (int g = 0; g < (two ? 2 : 1); ++g)
-                                for (int h = 0; h < C::H; ++h)
-                                    tma_load_3d(sQ + g * C::kTile + h * kBox, &maps.q, 64 * h, w.h * a.G, e.row0 + g * TM, &barQ);
-                        }
-                        __syncwarp();
-                    }
+                }
+                for (uint32_t i = Shape<kKT>(a, w, TM).stages; i > 0 && ok; --i, ++n, at = at.plus(1)) {  // the output's
+                    ok = wait_on(&barFree[at.s], at.ph ^ 1, a.err);
+                    if (ok && lane == 0) mbar_arrive(&barKV[at.s]);
                 }
             }
             // wait for the copies that no one consumed (only after a wait that gave up)
@@ -481,15 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 const uint64_t desc = tc::smem_desc_sw128(0, 16, 1024), desc_v = tc::smem_desc_sw128(0, kBox, 1024);
                 const uint64_t q_desc = desc + (smem_addr(sQ) >> 4), kv_addr = smem_addr(sKV) >> 4;
                 uint32_t u = 0, nFix = 0, nP[2] = {0, 0};
-                // positions in the ring: stage and phase of the tile's K (V follows), without divisions
-                struct Pos {
-                    uint32_t s, ph;
-                    __device__ __forceinline__ Pos plus(uint32_t k) const {
-                        const uint32_t t = s + k;
-                        return t >= C::kStages ? Pos{t - C::kStages, ph ^ 1u} : Pos{t, ph};
-                    }
-                };
-                Pos n{0, 0};
+                using Pos = Pos<C::kStages>;
+                Pos n;
                 auto wait_stage = [&](Pos i) { if (ok) ok = wait_on(&barKV[i.s], i.ph, a.err); };
                 auto free_stage = [&](Pos i) { tc::commit(&barFree[i.s]); };
                 // S_g = Q_q K^T with K at position i of the ring
@@ -511,17 +562,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 };
                 for (; more && ok; more = w.next(a, TQ), ++u) {
                     const PagedEntry& e = w.e;
-                    const bool pair = e.n <= TM;
+                    const Shape<kKT> sh(a, w, TM);
+                    const bool pair = sh.pair;
                     const int nt = w.t1 - w.t0, ahead = pair ? 2 : 1;  // a group's next tile
                     if (ok) ok = wait_on(&barQ, u & 1, a.err);
                     wait_stage(n);
-                    if (pair && nt > 1) wait_stage(n.plus(2));
                     if (!ok) break;
                     tc::fence_after_sync();
                     qk(0, 0, n);
                     if (pair) {
                         free_stage(n);
                         if (nt > 1) {
+                            wait_stage(n.plus(2));
+                            if (!ok) break;
+                            tc::fence_after_sync();
                             qk(1, 0, n.plus(2));
                             free_stage(n.plus(2));
                         }
@@ -560,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                             }
                         }
                     }
+                    n = n.plus(sh.stages);
                 }
                 tc::commit(&barDone);  // the issuing thread stays until its MMAs are done
                 wait_on(&barDone, 0, a.err);
@@ -568,46 +623,77 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             // -------------------------------------------------------- V of the masked tiles
             // They pass every stage of the ring (and hand it back with the MMAs), so that they can
             // neither run ahead of it nor fall behind it.
-            uint32_t n = 0, nFix = 0;
+            // The first of them also loads Q, as soon as the last unit's has been read.
+            uint32_t u = 0, nFix = 0;
+            Pos<C::kStages> at;
             const int f = tid - kFixWarp * 32;  // 0 .. 63
-            for (; more && ok; more = w.next(a, TQ)) {
+            for (; more && ok; more = w.next(a, TQ), ++u) {
                 const PagedEntry& e = w.e;
                 const int hi = e.last_pos();
-                for (int k = w.t0; k < w.t1 && ok; ++k, n += 2) {
+                const Shape<kKT> sh(a, w, TM);
+                if (warp == kFixWarp) {
+                    if (u > 0) ok = wait_on(&barQfree, (u - 1) & 1, a.err);
+                    if (ok && lane == 0) {
+                        const int tiles = sh.pair ? 1 : 2;
+                        mbar_arrive_expect_tx(&barQ, tiles * C::H * a.G * TM * 128);
+                        for (int g = 0; g < tiles; ++g)
+                            for (int h = 0; h < C::H; ++h)
+                                tma_load_3d(sQ + g * C::kTile + h * kBox, &maps.q, 64 * h, w.h * a.G, e.row0 + g * TM, &barQ);
+                    }
+                    __syncwarp();
+                }
+                for (int k = w.t0; k < w.t1 && ok; ++k) {
                     const int j0 = e.key_tile(k) * kKT;
-                    const uint32_t sk = n % C::kStages, s = (n + 1) % C::kStages;
-                    ok = wait_on(&barKV[sk], (n / C::kStages) & 1, a.err);
-                    if (ok && lane == 0) mbar_arrive(&barFree[sk]);
-                    if (ok) ok = wait_on(&barKV[s], ((n + 1) / C::kStages) & 1, a.err);
+                    ok = wait_on(&barKV[at.s], at.ph, a.err);
+                    if (ok && lane == 0) mbar_arrive(&barFree[at.s]);
+                    at = at.plus(1);
+                    if (ok) ok = wait_on(&barKV[at.s], at.ph, a.err);
                     if (!ok) break;
                     if (masked_tile(a, e, j0)) {
-                        unsigned char* sV = sKV + (size_t)s * C::kTile;
-                        const bool look = e.n > 1;  // (a single token's rows see the same keys)
-                        uint32_t inf = 0;           // exponents of all ones carry into the sign bits
-#pragma unroll 8
-                        for (int c = f; c < C::H * 128 * 8; c += 64) {
-                            const int j = j0 + ((c >> 3) & 127);
-                            uint4* at = reinterpret_cast<uint4*>(sV + (size_t)c * 16);
-                            if (!(j <= hi && (j >= e.lo || j < a.S))) {
-                                *at = make_uint4(0u, 0u, 0u, 0u);
-                            } else if (look) {
-                                const uint4 v = *at;
-                                inf |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
-                                       ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
-                            }
-                        }
-                        bool odd = (inf & 0x80008000u) != 0;
+                        unsigned char* sV = sKV + (size_t)at.s * C::kTile;
+                        // rows seen by some row of the unit: [0, n_sink) and [n_lo, n_hi)
+                        const int n_hi = max(0, min(kKT, hi - j0 + 1)), n_lo = max(0, min(n_hi, e.lo - j0));
+                        const int n_sink = a.W > 0 ? max(0, min(n_lo, a.S - j0)) : 0;
+                        auto zero = [&](int from, int to) {
+                            for (int c = 8 * from + f; c < 8 * to; c += 64)
+#pragma unroll
+                                for (int h = 0; h < C::H; ++h)
+                                    *reinterpret_cast<uint4*>(sV + h * kBox + (size_t)c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        };
+                        zero(n_sink, n_lo);
+                        zero(n_hi, kKT);
                         fence_proxy_async();
-                        odd = __any_sync(kFull, odd);
+                        uint32_t inf = 0;  // an exponent of all ones carries into its sign bit
+                        auto look = [&](int from, int to) {
+                            for (int c = 8 * from + f; c < 8 * to; c += 256)
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                                    for (int h = 0; h < C::H; ++h) {
+                                        const uint4 v = *reinterpret_cast<const uint4*>(sV + h * kBox + (size_t)min(c + 64 * y, 8 * to - 1) * 16);
+                                        inf |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                                               ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+                                    }
+                        };
+                        if (e.n > 1) {  // (a single token's rows see the same keys)
+                            look(0, n_sink);
+                            look(n_lo, n_hi);
+                        }
+                        const bool odd = __any_sync(kFull, (inf & 0x80008000u) != 0);
                         __syncwarp();
                         if (lane == 0) {
                             // (kFixDepth tiles on, the readers of this flag have passed: the ring holds fewer)
-                            dirty_sh[nFix % kFixDepth][warp - kFixWarp] = odd ? (int)s + 1 : 0;
+                            dirty_sh[nFix % kFixDepth][warp - kFixWarp] = odd ? (int)at.s + 1 : 0;
                             mbar_arrive(&barFix[nFix % kFixDepth]);
                         }
                         ++nFix;
                     }
-                    if (lane == 0) mbar_arrive(&barFree[s]);
+                    if (lane == 0) mbar_arrive(&barFree[at.s]);
+                    at = at.plus(1);
+                }
+                for (uint32_t i = sh.stages; i > 0 && ok; --i, at = at.plus(1)) {
+                    ok = wait_on(&barKV[at.s], at.ph, a.err);
+                    if (ok && lane == 0) mbar_arrive(&barFree[at.s]);
                 }
             }
         }
@@ -637,7 +723,7 @@ cudaError_t run(const PagedDims& m, const PagedArgs& a, const void* Q, const voi
     paged_chunk_kernel<D><<<workers, kThreads, C::kSmem, s>>>(maps, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_paged_merge<__nv_bfloat16, D, kKT>(a, 2 * TM, workers, 2 * TM * m.G, s);
+    return launch_paged_merge<__nv_bfloat16, D, kKT>(a, workers, std::min(2 * TM, m.max_new) * m.G, s);
 }
 
 }  // namespace

@@ -20,14 +20,23 @@ namespace cobs {
 
 constexpr int kErrBadLength = 3;  // lengths that contradict each other, the token rows or the table
 
+// What a worker leaves for the merge: its range in the sequence of tiles and the unit it begins in.
+struct alignas(16) PagedSeg {
+    long long b0, total;         // first tile, tiles in all
+    int count, head, t0, nt;     // tiles walked; the first unit's head, first tile and tiles
+    int row0, n, pos0, unused;   // the first unit's first token row, tokens, first position
+};
+
 struct PagedArgs {
     const int32_t* table;   // [R, max_pages]
     const int32_t* cu;      // [R + 1]
     const int32_t* kv_len;  // [R]
     float* lse;             // [n_tokens, Hq] or null
     void* O;                // [n_tokens, Hq, d]
-    float* rec;             // [workers][2][rec_rows][d + 4]: output, then running maximum (log2 units) and sum
-    int4* seg;              // [workers]: entry (request, tile of tokens), offset in the entry, tiles walked
+    float* rec;             // [workers][2] records: [d / 4][rec_rows][4] output (a warp's rows are contiguous),
+                            // then [rec_rows][2] running maximum (log2 units) and sum
+    PagedSeg* seg;          // [workers]
+    int rec_rows;
     int* err;
     int R, Hq, Hkv, G, page, page_shift, n_pages, max_pages, n_tokens, max_new, W, S;
     float sl2;              // log2(e) / sqrt(d)
@@ -86,9 +95,22 @@ struct PagedRange {
     int r, i;          // entry
     int off;           // tiles of the entry before it: head * nt + tile
     int count;
+    long long b0, total;
 };
 
-// Block-wide inclusive scan of one value per thread (T threads); tmp: T / 32 + 1 values.
+// total * w / n without a 64-bit division where the product is small
+__device__ __forceinline__ long long share_of(long long total, int w, int n) {
+    const unsigned long long x = (unsigned long long)total * (unsigned)w;
+    return x >> 32 ? (long long)(x / (unsigned)n) : (long long)((uint32_t)x / (uint32_t)n);
+}
+// the worker whose range holds tile x: ceil((x + 1) n / total) - 1
+__device__ __forceinline__ int worker_of(long long total, long long x, int n) {
+    const unsigned long long y = (unsigned long long)(x + 1) * (unsigned)n + (unsigned long long)total - 1;
+    return (int)((y | (unsigned long long)total) >> 32 ? y / (unsigned long long)total : (uint32_t)y / (uint32_t)total) - 1;
+}
+
+// Block-wide inclusive scan of one value per thread (T threads); tmp: T / 32 values, not the ones of the
+// scan just before.
 template <int T>
 __device__ __forceinline__ long long block_scan(long long v, long long* tmp, long long& total) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -107,16 +129,53 @@ __device__ __forceinline__ long long block_scan(long long v, long long* tmp, lon
         all += x;
     }
     total = all;
-    __syncthreads();
     return v + before;
 }
 
-// The ranges of workers w0 .. w0 + NW - 1 of n_workers, by all T threads of the block.
-// scratch: R + 1 ints; tmp: T / 32 long long; out: NW ranges (shared memory).
-template <int T, int KT, int NW>
-__device__ __forceinline__ void plan_ranges(const PagedArgs& a, int TQ, int w0, int n_workers, int* scratch,
-                                            long long* tmp, PagedRange* out) {
+// Worker w's range where every one of at most 32 requests is one entry: lane r of each warp looks after
+// request r, so no warp waits for another (a small call spends most of its time on such steps).
+// Returns whether the case is that one.
+template <int KT>
+__device__ __forceinline__ bool plan_small(const PagedArgs& a, int TQ, int w, int n_workers, PagedRange& out) {
+    if (a.R > 32) return false;
+    const int lane = threadIdx.x & 31;
+    int row0 = 0, n = 0, L = 0;
+    bool bad = false;
+    if (lane < a.R) request_of(a, lane, row0, n, L, bad);
+    if (__any_sync(kFull, n > TQ)) return false;
+    if (bad && w == 0) report_error(a.err, kErrBadLength);
+    const long long cost = n > 0 ? (long long)make_entry<KT>(a, lane, 0, TQ, row0, n, L).nt * a.Hkv : 0;
+    long long inc = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += u;
+    }
+    const long long total = __shfl_sync(kFull, inc, 31);
+    const long long b0 = share_of(total, w, n_workers), b1 = share_of(total, w + 1, n_workers);
+    const unsigned at = __ballot_sync(kFull, b0 >= inc - cost && b0 < inc);
+    out = PagedRange{0, 0, 0, 0, b0, total};
+    if (b1 > b0) {
+        out.r = __ffs(at) - 1;
+        out.off = (int)(b0 - __shfl_sync(kFull, inc - cost, out.r));
+        out.count = (int)(b1 - b0);
+    }
+    return true;
+}
+
+// Worker w's range, by all T threads of the block. scratch: R + 1 ints; tmp: 2 T / 32 values.
+template <int T, int KT>
+__device__ __forceinline__ void plan_range(const PagedArgs& a, int TQ, int w, int n_workers, int* scratch,
+                                           long long* tmp, PagedRange* out) {
+    PagedRange small;
+    if (plan_small<KT>(a, TQ, w, n_workers, small)) {
+        if (threadIdx.x == 0) *out = small;
+        __syncthreads();
+        return;
+    }
     const int tid = threadIdx.x;
+    int turn = 0;  // the scans' halves of tmp
+    auto scan = [&](long long v, long long& tot) { return block_scan<T>(v, tmp + (turn ^= 1) * (T / 32), tot); };
     // entries before each request
     long long base = 0;
     for (int r0 = 0; r0 < a.R; r0 += T) {
@@ -124,23 +183,24 @@ __device__ __forceinline__ void plan_ranges(const PagedArgs& a, int TQ, int w0, 
         int row0, n = 0, L;
         bool bad = false;
         if (r < a.R) request_of(a, r, row0, n, L, bad);
-        if (bad && w0 == 0) report_error(a.err, kErrBadLength);
+        if (bad && w == 0) report_error(a.err, kErrBadLength);
         long long tot;
-        const long long inc = block_scan<T>((n + TQ - 1) / TQ, tmp, tot);
+        const long long inc = scan((n + TQ - 1) / TQ, tot);
         if (r < a.R) scratch[r + 1] = (int)(base + inc);
         base += tot;
     }
-    if (tid == 0) scratch[0] = 0;
-    if (tid < NW) out[tid] = PagedRange{0, 0, 0, 0};
+    if (tid == 0) {
+        scratch[0] = 0;
+        *out = PagedRange{0, 0, 0, 0, 0, 0};
+    }
     __syncthreads();
     const int E = (int)base;
     auto cost_of = [&](int e, int& r, int& i) -> int {
         int lo = 0, hi = a.R - 1;  // the last request whose first entry is <= e
-        while (lo < hi) {
+        while (lo < hi) {          // (requests without entries share their successor's number)
             const int mid = (lo + hi + 1) >> 1;
             if (scratch[mid] <= e) lo = mid; else hi = mid - 1;
         }
-        // (requests without entries share their successor's prefix: the last one of equals holds e)
         int row0, n, L;
         bool bad;
         request_of(a, lo, row0, n, L, bad);
@@ -154,23 +214,20 @@ __device__ __forceinline__ void plan_ranges(const PagedArgs& a, int TQ, int w0, 
     for (int e0 = 0; e0 < E; e0 += T) {
         cost = e0 + tid < E ? cost_of(e0 + tid, r, i) : 0;
         long long tot;
-        inc = block_scan<T>(cost, tmp, tot);
+        inc = scan(cost, tot);
         total += tot;
     }
+    const long long b0 = share_of(total, w, n_workers), b1 = share_of(total, w + 1, n_workers);
     long long before = 0;
     for (int e0 = 0; e0 < E; e0 += T) {
         if (E > T) {  // else the values of the only round above still stand
             cost = e0 + tid < E ? cost_of(e0 + tid, r, i) : 0;
             long long tot;
-            inc = block_scan<T>(cost, tmp, tot) + before;
+            inc = scan(cost, tot) + before;
             before += tot;
         }
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const long long b0 = total * (w0 + w) / n_workers, b1 = total * (w0 + w + 1) / n_workers;
-            if (b1 > b0 && b0 >= inc - cost && b0 < inc)
-                out[w] = PagedRange{r, i, (int)(b0 - (inc - cost)), (int)(b1 - b0)};
-        }
+        if (b1 > b0 && b0 >= inc - cost && b0 < inc)
+            *out = PagedRange{r, i, (int)(b0 - (inc - cost)), (int)(b1 - b0), b0, total};
     }
     __syncthreads();
 }
@@ -217,6 +274,11 @@ struct PagedWalk {
         return true;
     }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == e.nt; }
+    // what the merge has to know (after first(); count 0: no range)
+    __device__ __forceinline__ PagedSeg seg(const PagedRange& g) const {
+        if (g.count == 0) return PagedSeg{g.b0, g.total, 0, 0, 0, 0, 0, 0, 0, 0};
+        return PagedSeg{g.b0, g.total, g.count, h, t0, e.nt, e.row0, e.n, e.pos0, 0};
+    }
 };
 
 // Page that holds key tokens [j, j + page): -1 behind the table, or (reported) outside the cache.
@@ -231,109 +293,92 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int r, int slot, bool
 }
 
 // Joins the records of every unit that range boundaries cut. Block (c, y): boundary c (the start of
-// worker c's range) if it is the first one inside its unit; the unit's rows 4 y + warp, then every
-// 4 gridDim.y, one warp each. Lane i looks after piece i (32 at a time): the pieces' tile counts,
-// maxima and sums come in one round trip each, then the outputs without waiting on one another.
-// Pieces lie in the order of the workers, so the order of the sums is fixed.
+// worker c's range) if it is the first one inside its unit, and the unit's rows 8 y .. 8 y + 7.
+// Which workers hold the pieces follows from the equal division alone, so after the segment's one
+// round trip come the pieces' maxima and sums, then their outputs without waiting on one another.
+// Pieces are added in the order of the workers.
+constexpr int kMaxWorkers = 512;
+
 template <typename T, int D, int KT>
-__global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int TQ, int n_workers, int rec_rows) {
+__global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int n_workers) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int4 s = a.seg[c], before = a.seg[c - 1];
-    if (s.w == 0) return;
-    int row_r, n_r, L_r;
-    bool bad;
-    request_of(a, s.x, row_r, n_r, L_r, bad);
-    const PagedEntry e = make_entry<KT>(a, s.x, s.y, TQ, row_r, n_r, L_r);
-    const int h = s.z / e.nt, t0 = s.z - h * e.nt;
-    if (t0 == 0) return;
-    // the last worker before with tiles (some have none where there are fewer tiles than workers)
-    int p = c - 1;
-    int4 q = before;
-    while (p > 0 && q.w == 0) q = a.seg[--p];
-    const bool same = q.x == s.x && q.y == s.y && q.z / e.nt == h;
-    if (same && q.z - h * e.nt > 0) return;  // an earlier boundary inside this unit
-    constexpr int C = D / 32;
-    for (int row = blockIdx.y * 4 + warp; row < e.n * a.G; row += gridDim.y * 4) {
-        float M = -INFINITY, l = 0.0f, o[C];
-#pragma unroll
-        for (int k = 0; k < C; ++k) o[k] = 0.0f;
-        int covered = t0;      // tiles of the unit in the pieces up to worker w0 - 1 (the first one's end at t0)
-        for (int w0 = p; w0 < n_workers; w0 += 32) {
-            const int w = w0 + lane;
-            const int tiles = w > p && w < n_workers ? a.seg[w].w : 0;
-            int inc = tiles;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int u = __shfl_up_sync(kFull, inc, d);
-                if (lane >= d) inc += u;
-            }
-            // a piece: the first worker, and those whose range begins before the unit's end
-            const bool piece = w == p || (tiles > 0 && covered + inc - tiles < e.nt);
-            const float* rec = a.rec + (((size_t)w * 2 + (w == p && !same ? 1 : 0)) * rec_rows + row) * (D + 4);
-            const float m1 = piece ? rec[D] : -INFINITY, l1 = piece ? rec[D + 1] : 0.0f;
-            float nm = m1;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(kFull, nm, d));
-            nm = fmaxf(nm, M);
-            const float f0 = M == -INFINITY ? 0.0f : exp2f(M - nm);
-            // (a piece of NaN scores alone has a sum and no maximum: NaN then)
-            const float f1 = m1 == -INFINITY && l1 == 0.0f ? 0.0f : exp2f(m1 - nm);
-            float sum = l1 * f1;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
-            l = l * f0 + sum;
-#pragma unroll
-            for (int k = 0; k < C; ++k) o[k] *= f0;
-            M = nm;
-            const unsigned who = __ballot_sync(kFull, piece && f1 != 0.0f);  // (NaN counts)
-            const int first = __ffs(who) - 1, last = 31 - __clz(who);
-            if (who) {
-#pragma unroll 8
-                for (int i = first; i <= last; ++i) {
-                    const float f = __shfl_sync(kFull, f1, i);
-                    if (!(who >> i & 1u)) continue;
-                    const float* src = a.rec + (((size_t)(w0 + i) * 2 + (w0 + i == p && !same ? 1 : 0)) * rec_rows + row) * (D + 4) + lane * C;
-                    float v[C];
-                    if constexpr (C == 4) {
-                        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-                    } else {
-                        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
-                    }
-#pragma unroll
-                    for (int k = 0; k < C; ++k) o[k] = fmaf(v[k], f, o[k]);
-                }
-            }
-            covered += __shfl_sync(kFull, inc, 31);
-            if (covered >= e.nt) break;
-        }
-        const int tok = row / a.G;
-        const size_t orow = (size_t)(e.row0 + tok) * a.Hq + h * a.G + row % a.G;
-        const bool empty = e.pos0 + tok < 0;
-        const float inv = 1.0f / l;
-#pragma unroll
-        for (int k = 0; k < C; ++k)
-            Elem<T>::store(static_cast<T*>(a.O) + orow * D + lane * C + k, empty ? 0.0f : o[k] * inv);
-        if (a.lse && lane == 0) a.lse[orow] = empty ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+    __shared__ float2 ml[kMaxWorkers][8];
+    const int c = blockIdx.x + 1, tid = threadIdx.x;
+    const PagedSeg s = a.seg[c];
+    const int row = blockIdx.y * 8 + (tid & 7), q = tid >> 3;
+    if (s.count == 0 || s.t0 == 0 || blockIdx.y * 8 >= s.n * a.G) return;
+    const long long U0 = s.b0 - s.t0, U1 = U0 + s.nt;
+    const int f = worker_of(s.total, U0, n_workers), l = worker_of(s.total, U1 - 1, n_workers);
+    if (worker_of(s.total, s.b0 - 1, n_workers) != f) return;  // an earlier boundary inside this unit
+    const bool begins = share_of(s.total, f, n_workers) == U0;  // the first piece begins its worker's range
+    const int rows = a.rec_rows;
+    const size_t size = (size_t)rows * (D + 2);
+    auto record = [&](int w) { return a.rec + ((size_t)w * 2 + (w == f && !begins ? 1 : 0)) * size; };
+    for (int w = f + q; w <= l; w += 16) {
+        const bool some = share_of(s.total, w + 1, n_workers) > share_of(s.total, w, n_workers);
+        ml[w - f][tid & 7] = some && row < s.n * a.G ? reinterpret_cast<const float2*>(record(w) + (size_t)rows * D)[row]
+                                                    : make_float2(-INFINITY, 0.0f);
     }
+    __syncthreads();
+    if (row >= s.n * a.G) return;
+    float M = -INFINITY;
+    for (int w = 0; w <= l - f; ++w) M = fmaxf(M, ml[w][tid & 7].x);
+    constexpr int C = D / 64;  // float4 columns per thread
+    float sum = 0.0f;
+    float4 o[C];
+#pragma unroll
+    for (int k = 0; k < C; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int w = 0; w <= l - f; ++w) {
+        const float2 x = ml[w][tid & 7];
+        if (x.x == -INFINITY && x.y == 0.0f) continue;
+        const float g = exp2f(x.x - M);  // (a piece of NaN scores alone has a sum and no maximum: NaN)
+        sum = fmaf(x.y, g, sum);
+        const float4* v = reinterpret_cast<const float4*>(record(f + w)) + row;
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const float4 y = v[(size_t)(q + 16 * k) * rows];
+            o[k].x = fmaf(y.x, g, o[k].x);
+            o[k].y = fmaf(y.y, g, o[k].y);
+            o[k].z = fmaf(y.z, g, o[k].z);
+            o[k].w = fmaf(y.w, g, o[k].w);
+        }
+    }
+    const int tok = row / a.G;
+    const size_t orow = (size_t)(s.row0 + tok) * a.Hq + s.head * a.G + row - tok * a.G;
+    const bool empty = s.pos0 + tok < 0;
+    const float inv = 1.0f / sum;
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+        T* out = static_cast<T*>(a.O) + orow * D + 4 * (q + 16 * k);
+        float v[4] = {o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv};
+        if (empty) v[0] = v[1] = v[2] = v[3] = 0.0f;
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        } else {
+            *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    if (a.lse && q == 0) a.lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
-// The merge after an attention grid of `workers` ranges, as its programmatic dependent (its launch
-// overlaps the grid's tail).
+// The merge after an attention grid of `workers` ranges whose units have at most `rows` rows, as its
+// programmatic dependent (its launch overlaps the grid's tail).
 template <typename T, int D, int KT>
-cudaError_t launch_paged_merge(const PagedArgs& a, int TQ, int workers, int rec_rows, cudaStream_t s) {
+cudaError_t launch_paged_merge(const PagedArgs& a, int workers, int rows, cudaStream_t s) {
     if (workers < 2) return cudaSuccess;
+    if (workers > kMaxWorkers) return cudaErrorInvalidValue;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(workers - 1, (rec_rows + 15) / 16);
+    cfg.gridDim = dim3(workers - 1, (rows + 7) / 8);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, KT>, a, TQ, workers, rec_rows);
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, KT>, a, workers);
 }
 
 }  // namespace cobs

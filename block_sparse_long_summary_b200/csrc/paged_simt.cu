@@ -39,7 +39,7 @@ template <int D, int M>
 __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const float* Q, long long q_stride,
                                                         const float* kc, const float* vc) {
     extern __shared__ __align__(16) float sm[];
-    __shared__ long long tmp[kT / 32];
+    __shared__ long long tmp[2 * kT / 32];
     __shared__ PagedRange range;
     __shared__ int page_sh[2][kKT / 16];
     constexpr int RM = M / 16, CD = D / 16, KS = D + 4;
@@ -49,12 +49,13 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const float
     float* sP = sV + kKT * D;     // [M][68]
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int TQ = M / a.G;
-    plan_ranges<kT, kKT, 1>(a, TQ, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm), tmp, &range);
+    plan_range<kT, kKT>(a, TQ, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm), tmp, &range);
     const PagedRange g = range;
-    if (tid == 0) a.seg[blockIdx.x] = make_int4(g.r, g.i, g.off, g.count);
     PagedWalk<kKT> w;
     int piece = 0;
-    for (bool more = w.first(a, TQ, g); more; more = w.next(a, TQ), ++piece) {
+    bool more = w.first(a, TQ, g);
+    if (tid == 0) a.seg[blockIdx.x] = w.seg(g);
+    for (; more; more = w.next(a, TQ), ++piece) {
         const PagedEntry& e = w.e;
         const int rows = e.n * a.G, hi = e.last_pos();
         const int ppt = kKT >> a.page_shift;  // pages per tile (0: a page holds two tiles)
@@ -185,25 +186,24 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const float
             for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
             const int row = ty + 16 * y;
             if (row >= rows) continue;
-            float* dst;
+            float4* dst;
+            size_t step = 16;  // float4 from one 64-column group to the next
             float f = 1.0f;
             if (whole) {
                 const size_t orow = (size_t)(e.row0 + row / a.G) * a.Hq + w.h * a.G + row % a.G;
                 const bool empty = pos[y] < 0;
-                dst = static_cast<float*>(a.O) + orow * D;
+                dst = reinterpret_cast<float4*>(static_cast<float*>(a.O) + orow * D) + tx;
                 f = empty ? 0.0f : 1.0f / sum;
                 if (a.lse && tx == 0) a.lse[orow] = empty ? -INFINITY : (m[y] + log2f(sum)) * 0.6931471805599453f;
             } else {
-                dst = a.rec + (((size_t)blockIdx.x * 2 + slot) * M + row) * (D + 4);
-                if (tx == 0) {
-                    dst[D] = m[y];
-                    dst[D + 1] = sum;
-                }
+                float* rec = a.rec + ((size_t)blockIdx.x * 2 + slot) * M * (D + 2);
+                dst = reinterpret_cast<float4*>(rec) + tx * M + row;
+                step = 16 * M;
+                if (tx == 0) reinterpret_cast<float2*>(rec + (size_t)M * D)[row] = make_float2(m[y], sum);
             }
 #pragma unroll
             for (int x = 0; x < CD; x += 4)
-                *reinterpret_cast<float4*>(dst + (x / 4) * 64 + tx * 4) =
-                    make_float4(o[y][x] * f, o[y][x + 1] * f, o[y][x + 2] * f, o[y][x + 3] * f);
+                dst[(x / 4) * step] = make_float4(o[y][x] * f, o[y][x + 1] * f, o[y][x + 2] * f, o[y][x + 3] * f);
         }
     }
 }
@@ -217,7 +217,7 @@ cudaError_t run(const PagedArgs& a, int workers, const float* Q, long long q_str
     paged_simt_kernel<D, M><<<workers, kT, smem, s>>>(a, Q, q_stride, kc, vc);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_paged_merge<float, D, kKT>(a, M / a.G, workers, M, s);
+    return launch_paged_merge<float, D, kKT>(a, workers, std::min(M / a.G, a.max_new) * a.G, s);
 }
 
 }  // namespace

@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kTT) paged_tables_kernel(TableArgs a) {
     extern __shared__ int sh[];
     int* s_tok = sh;               // [R + 1] tokens before each request
     int* s_pg = sh + a.R + 1;      // [R] pages handed out before each request, less its open pages
-    __shared__ long long tmp[kTT / 32];
+    __shared__ long long tmp[2][kTT / 32];
     const int tid = threadIdx.x;
     const bool lead = blockIdx.x == 0;
     const int P = 1 << a.page_shift;
@@ -50,13 +50,13 @@ __global__ void __launch_bounds__(kTT) paged_tables_kernel(TableArgs a) {
         // the token rows at once), pages above
         n = min(n, a.n_tokens + 1);
         long long all;
-        long long inc = block_scan<kTT>(n, tmp, all);
+        long long inc = block_scan<kTT>(n, tmp[0], all);
         const long long before = tok + inc - n;
         const int fit = (int)min((long long)n, max(0ll, a.n_tokens - before));  // more tokens than rows: cut off
         if (fit < n && lead) report_error(a.err, kErrBadLength);
         const int open = (c + P - 1) >> a.page_shift, end = (int)(((long long)c + fit + P - 1) >> a.page_shift);
         long long taken;
-        const long long pinc = block_scan<kTT>(end - open, tmp, taken);
+        const long long pinc = block_scan<kTT>(end - open, tmp[1], taken);
         if (r < a.R) {
             s_tok[r] = (int)min(before, (long long)a.n_tokens);
             s_pg[r] = (int)(pages + pinc - (end - open)) - open;
