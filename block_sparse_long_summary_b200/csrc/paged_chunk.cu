@@ -68,24 +68,25 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// 32 columns into s[base ..], without waiting
-template <int BASE>
-__device__ __forceinline__ void ld32_at(uint32_t taddr, float (&s)[kKT]) {
+// 32 columns into s, without waiting
+__device__ __forceinline__ void ld32_to(uint32_t taddr, float (&s)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=f"(s[BASE + 0]), "=f"(s[BASE + 1]), "=f"(s[BASE + 2]), "=f"(s[BASE + 3]), "=f"(s[BASE + 4]), "=f"(s[BASE + 5]),
-          "=f"(s[BASE + 6]), "=f"(s[BASE + 7]), "=f"(s[BASE + 8]), "=f"(s[BASE + 9]), "=f"(s[BASE + 10]), "=f"(s[BASE + 11]),
-          "=f"(s[BASE + 12]), "=f"(s[BASE + 13]), "=f"(s[BASE + 14]), "=f"(s[BASE + 15]), "=f"(s[BASE + 16]), "=f"(s[BASE + 17]),
-          "=f"(s[BASE + 18]), "=f"(s[BASE + 19]), "=f"(s[BASE + 20]), "=f"(s[BASE + 21]), "=f"(s[BASE + 22]), "=f"(s[BASE + 23]),
-          "=f"(s[BASE + 24]), "=f"(s[BASE + 25]), "=f"(s[BASE + 26]), "=f"(s[BASE + 27]), "=f"(s[BASE + 28]), "=f"(s[BASE + 29]),
-          "=f"(s[BASE + 30]), "=f"(s[BASE + 31])
+        : "=f"(s[0]), "=f"(s[1]), "=f"(s[2]), "=f"(s[3]), "=f"(s[4]), "=f"(s[5]), "=f"(s[6]), "=f"(s[7]), "=f"(s[8]), "=f"(s[9]),
+          "=f"(s[10]), "=f"(s[11]), "=f"(s[12]), "=f"(s[13]), "=f"(s[14]), "=f"(s[15]), "=f"(s[16]), "=f"(s[17]), "=f"(s[18]),
+          "=f"(s[19]), "=f"(s[20]), "=f"(s[21]), "=f"(s[22]), "=f"(s[23]), "=f"(s[24]), "=f"(s[25]), "=f"(s[26]), "=f"(s[27]),
+          "=f"(s[28]), "=f"(s[29]), "=f"(s[30]), "=f"(s[31])
         : "r"(taddr));
 }
-// After wait_ld: the 32 registers are not to be used before this point.
-__device__ __forceinline__ void touch32(float (&s)[kKT], const int base) {
+// The registers of a load are not to be used before the wait for it.
+__device__ __forceinline__ void touch32(float (&s)[32]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(s[base + j]));
+    for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(s[j]));
+}
+__device__ __forceinline__ void wait_ld32(float (&s)[32]) {
+    tc::wait_ld();
+    touch32(s);
 }
 __device__ __forceinline__ float ld1(uint32_t taddr) {
     float v;
@@ -99,8 +100,6 @@ template <int N> __device__ __forceinline__ void rows_sync(int id) { asm volatil
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
 }
-template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // Bounded wait without a suspend hint: with one, a poll of a phase that is already complete costs 46
 // cycles, without 15 (clock64 around completed phases), and most waits here find theirs complete.
@@ -235,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     if (warp < 8) {
         // ------------------------------------------------------------ softmax and epilogue of row tile g
         // (after a wait that gave up these warps go on without waiting: they meet at named barriers)
-        reg_inc<216>();
         const int g = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + 128 * g, tO = tmem + lanes + kColO + 128 * g;
@@ -270,26 +268,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 }
                 tc::fence_after_sync();
                 if (warp_live) {
-                    float s[kKT];
-                    ld32_at<0>(tS, s);
-                    ld32_at<32>(tS + 32, s);
-                    ld32_at<64>(tS + 64, s);
-                    ld32_at<96>(tS + 96, s);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int c = 0; c < kKT; c += 32) touch32(s, c);
                     const int hi = t - j0, lo = a.W > 0 ? hi - a.W + 1 : 0, sk = a.W > 0 ? a.S - j0 : 0;
-                    if (masked) {
-#pragma unroll
+                    if (masked) {  // the scores this row does not see: -infinity, in place
+#pragma unroll 1
                         for (int c = 0; c < kKT; c += 32) {
                             const uint32_t see = bits_below(hi - c + 1) & (~bits_below(lo - c) | bits_below(sk - c));
+                            float s[32];
+                            ld32_to(tS + c, s);
+                            wait_ld32(s);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) s[c + j] = see & (1u << j) ? s[c + j] : -INFINITY;
+                            for (int j = 0; j < 32; ++j) s[j] = see & (1u << j) ? s[j] : -INFINITY;
+                            tc::st32(tS + c, s);
                         }
+                        tc::wait_st();
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int c = 0; c < kKT; c += 64) {
+                        float s[32], s1[32];
+                        ld32_to(tS + c, s);
+                        ld32_to(tS + c + 32, s1);
+                        wait_ld32(s);
+                        touch32(s1);
 #pragma unroll
-                    for (int j = 0; j < kKT; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], s[j], s[j + 1]);
+                        for (int j = 0; j < 32; j += 2) {
+                            mx[j & 2] = max3(mx[j & 2], s[j], s[j + 1]);
+                            mx[(j & 2) + 1] = max3(mx[(j & 2) + 1], s1[j], s1[j + 1]);
+                        }
+                    }
                     const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                     const bool grow = mt > m + 8.0f;  // (from -infinity too; never for a row that sees nothing)
                     if (k > kg && __any_sync(kFull, grow && m != -INFINITY)) {
@@ -298,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             float o[32];
-                            tc::ld32(tO + c, o);
-                            tc::wait_ld();
+                            ld32_to(tO + c, o);
+                            wait_ld32(o);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] *= f;
                             tc::st32(tO + c, o);
@@ -308,20 +314,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     }
                     if (grow) m = mt;
                     const float neg = m == -INFINITY ? 0.0f : -m;
+                    // p = 2^(s c - m) of 32 keys at a time, the next ones on their way from TMEM: P, half as
+                    // wide, follows behind the scores still to be read. The loops stay rolled: unrolled over
+                    // the 128 keys the code outgrew the instruction caches and every pass waited for it.
                     float2 ps[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     const float2 scale = make_float2(sl2, sl2), shift = make_float2(neg, neg);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    auto powers = [&](const float (&s)[32], int c) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            float2 x = fma2(make_float2(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), scale, shift);
+                            float2 x = fma2(make_float2(s[2 * j], s[2 * j + 1]), scale, shift);
                             x.x = tc::ex2(x.x);
                             x.y = tc::ex2(x.y);
                             ps[j & 1] = add2(ps[j & 1], x);
                             pk[j] = pack_bf16(x.x, x.y);
                         }
-                        if (!dirty) st16(tS + 16 * c, pk);
+                        if (!dirty) st16(tS + c / 2, pk);
+                    };
+                    {
+                        float s[32], s1[32];
+                        ld32_to(tS, s);
+#pragma unroll 1
+                        for (int c = 0; c < kKT; c += 64) {
+                            wait_ld32(s);
+                            ld32_to(tS + c + 32, s1);
+                            powers(s, c);
+                            wait_ld32(s1);
+                            if (c + 64 < kKT) ld32_to(tS + c + 64, s);
+                            powers(s1, c + 32);
+                        }
                     }
                     ps[0] = add2(ps[0], ps[1]);
                     l += ps[0].x + ps[0].y;
@@ -334,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                         for (int c = 0; c < D; c += 32) {
                             float o[32];
                             if (k > kg) {
-                                tc::ld32(tO + c, o);
-                                tc::wait_ld();
+                                ld32_to(tO + c, o);
+                                wait_ld32(o);
                             } else {
 #pragma unroll
                                 for (int j = 0; j < 32; ++j) o[j] = 0.0f;
@@ -414,14 +435,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll 1
                     for (int c = c0; c < c1; c += 32) {
                         float o[32];
-                        tc::ld32((both ? tmem + lanes + kColO : tO) + c, o);
-                        tc::wait_ld();
+                        ld32_to((both ? tmem + lanes + kColO : tO) + c, o);
+                        wait_ld32(o);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) o[j] = f0 != 0.0f ? o[j] * f0 : 0.0f;
                         if (both) {
                             float o1[32];
-                            tc::ld32(tmem + lanes + kColO + 128 + c, o1);
-                            tc::wait_ld();
+                            ld32_to(tmem + lanes + kColO + 128 + c, o1);
+                            wait_ld32(o1);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] = f1 != 0.0f ? fmaf(o1[j], f1, o[j]) : o[j];
                         }
@@ -483,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
-        reg_dec<72>();
         if (warp == kLoadWarp) {
             // -------------------------------------------------------- loads
             const int shift = 7 - a.page_shift, ppt = 1 << shift, per = 32 >> shift;  // pages per tile, tiles per look-up
