@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     bool ok = true;
     PagedWalk<kKT> w;
     bool more = w.first(a, TQ, rg);
-    if (tid == kFixWarp * 32) a.seg[blockIdx.x] = w.seg(rg);
+    if (tid == kFixWarp * 32 + 32) a.seg[blockIdx.x] = w.seg(a, rg, blockIdx.x);
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax and epilogue of row tile g
@@ -718,7 +718,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             }
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -743,7 +742,7 @@ cudaError_t run(const PagedDims& m, const PagedArgs& a, const void* Q, const voi
     paged_chunk_kernel<D><<<workers, kThreads, C::kSmem, s>>>(maps, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_paged_merge<__nv_bfloat16, D, kKT>(a, workers, std::min(2 * TM, m.max_new) * m.G, s);
+    return launch_paged_merge<__nv_bfloat16, D>(a, workers, std::min(2 * TM, m.max_new) * m.G, s);
 }
 
 }  // namespace

@@ -20,11 +20,12 @@ namespace cobs {
 
 constexpr int kErrBadLength = 3;  // lengths that contradict each other, the token rows or the table
 
-// What a worker leaves for the merge: its range in the sequence of tiles and the unit it begins in.
+// What a worker leaves for the merge about the boundary at which its range begins: the unit that the
+// boundary cuts, if it is the first one to, and the workers whose ranges hold its pieces.
 struct alignas(16) PagedSeg {
-    long long b0, total;         // first tile, tiles in all
-    int count, head, t0, nt;     // tiles walked; the first unit's head, first tile and tiles
-    int row0, n, pos0, unused;   // the first unit's first token row, tokens, first position
+    int rows;               // rows of the unit (0: nothing to join at this boundary)
+    int first, last, slot;  // workers of the pieces, and the first one's record (0 or 1)
+    int row0, pos0, head, unused;  // the unit's first token row and position, its head
 };
 
 struct PagedArgs {
@@ -95,7 +96,8 @@ struct PagedRange {
     int r, i;          // entry
     int off;           // tiles of the entry before it: head * nt + tile
     int count;
-    long long b0, total;
+    long long b0, total;  // first tile, tiles in all
+    int workers;       // that have a range: at most one per tile
 };
 
 // total * w / n without a 64-bit division where the product is small
@@ -107,6 +109,13 @@ __device__ __forceinline__ long long share_of(long long total, int w, int n) {
 __device__ __forceinline__ int worker_of(long long total, long long x, int n) {
     const unsigned long long y = (unsigned long long)(x + 1) * (unsigned)n + (unsigned long long)total - 1;
     return (int)((y | (unsigned long long)total) >> 32 ? y / (unsigned long long)total : (uint32_t)y / (uint32_t)total) - 1;
+}
+
+// 2^x on the special-function unit (approximate, flush-to-zero)
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Block-wide inclusive scan of one value per thread (T threads); tmp: T / 32 values, not the ones of the
@@ -152,11 +161,12 @@ __device__ __forceinline__ bool plan_small(const PagedArgs& a, int TQ, int w, in
         if (lane >= o) inc += u;
     }
     const long long total = __shfl_sync(kFull, inc, 31);
-    const long long b0 = share_of(total, w, n_workers), b1 = share_of(total, w + 1, n_workers);
-    const unsigned at = __ballot_sync(kFull, b0 >= inc - cost && b0 < inc);
-    out = PagedRange{0, 0, 0, 0, b0, total};
-    if (b1 > b0) {
-        out.r = __ffs(at) - 1;
+    const int n_eff = (int)min((long long)n_workers, total);
+    out = PagedRange{0, 0, 0, 0, 0, total, n_eff};
+    if (w < n_eff) {
+        const long long b0 = share_of(total, w, n_eff), b1 = share_of(total, w + 1, n_eff);
+        out.b0 = b0;
+        out.r = __ffs(__ballot_sync(kFull, b0 >= inc - cost && b0 < inc)) - 1;
         out.off = (int)(b0 - __shfl_sync(kFull, inc - cost, out.r));
         out.count = (int)(b1 - b0);
     }
@@ -191,7 +201,7 @@ __device__ __forceinline__ void plan_range(const PagedArgs& a, int TQ, int w, in
     }
     if (tid == 0) {
         scratch[0] = 0;
-        *out = PagedRange{0, 0, 0, 0, 0, 0};
+        *out = PagedRange{0, 0, 0, 0, 0, 0, 0};
     }
     __syncthreads();
     const int E = (int)base;
@@ -217,7 +227,9 @@ __device__ __forceinline__ void plan_range(const PagedArgs& a, int TQ, int w, in
         inc = scan(cost, tot);
         total += tot;
     }
-    const long long b0 = share_of(total, w, n_workers), b1 = share_of(total, w + 1, n_workers);
+    const int n_eff = (int)min((long long)n_workers, total);
+    if (w >= n_eff) return;  // (the whole block)
+    const long long b0 = share_of(total, w, n_eff), b1 = share_of(total, w + 1, n_eff);
     long long before = 0;
     for (int e0 = 0; e0 < E; e0 += T) {
         if (E > T) {  // else the values of the only round above still stand
@@ -226,8 +238,8 @@ __device__ __forceinline__ void plan_range(const PagedArgs& a, int TQ, int w, in
             inc = scan(cost, tot) + before;
             before += tot;
         }
-        if (b1 > b0 && b0 >= inc - cost && b0 < inc)
-            *out = PagedRange{r, i, (int)(b0 - (inc - cost)), (int)(b1 - b0), b0, total};
+        if (b0 >= inc - cost && b0 < inc)
+            *out = PagedRange{r, i, (int)(b0 - (inc - cost)), (int)(b1 - b0), b0, total, n_eff};
     }
     __syncthreads();
 }
@@ -274,10 +286,20 @@ struct PagedWalk {
         return true;
     }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == e.nt; }
-    // what the merge has to know (after first(); count 0: no range)
-    __device__ __forceinline__ PagedSeg seg(const PagedRange& g) const {
-        if (g.count == 0) return PagedSeg{g.b0, g.total, 0, 0, 0, 0, 0, 0, 0, 0};
-        return PagedSeg{g.b0, g.total, g.count, h, t0, e.nt, e.row0, e.n, e.pos0, 0};
+    // what the merge has to know (after first()): worker w's boundary
+    __device__ __forceinline__ PagedSeg seg(const PagedArgs& a, const PagedRange& g, int w) const {
+        PagedSeg s{};
+        if (g.count == 0 || t0 == 0) return s;
+        const long long U0 = g.b0 - t0;
+        s.first = worker_of(g.total, U0, g.workers);
+        if (s.first != w - 1) return s;  // an earlier boundary inside this unit
+        s.last = worker_of(g.total, U0 + e.nt - 1, g.workers);
+        s.slot = share_of(g.total, s.first, g.workers) == U0 ? 0 : 1;
+        s.rows = e.n * a.G;
+        s.row0 = e.row0;
+        s.pos0 = e.pos0;
+        s.head = h;
+        return s;
     }
 };
 
@@ -293,64 +315,87 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int r, int slot, bool
 }
 
 // Joins the records of every unit that range boundaries cut. Block (c, y): boundary c (the start of
-// worker c's range) if it is the first one inside its unit, and the unit's rows 8 y .. 8 y + 7.
-// Which workers hold the pieces follows from the equal division alone, so after the segment's one
-// round trip come the pieces' maxima and sums, then their outputs without waiting on one another.
-// Pieces are added in the order of the workers.
-constexpr int kMaxWorkers = 512;
-
-template <typename T, int D, int KT>
-__global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int n_workers) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ float2 ml[kMaxWorkers][8];
-    const int c = blockIdx.x + 1, tid = threadIdx.x;
-    const PagedSeg s = a.seg[c];
-    const int row = blockIdx.y * 8 + (tid & 7), q = tid >> 3;
-    if (s.count == 0 || s.t0 == 0 || blockIdx.y * 8 >= s.n * a.G) return;
-    const long long U0 = s.b0 - s.t0, U1 = U0 + s.nt;
-    const int f = worker_of(s.total, U0, n_workers), l = worker_of(s.total, U1 - 1, n_workers);
-    if (worker_of(s.total, s.b0 - 1, n_workers) != f) return;  // an earlier boundary inside this unit
-    const bool begins = share_of(s.total, f, n_workers) == U0;  // the first piece begins its worker's range
-    const int rows = a.rec_rows;
-    const size_t size = (size_t)rows * (D + 2);
-    auto record = [&](int w) { return a.rec + ((size_t)w * 2 + (w == f && !begins ? 1 : 0)) * size; };
-    for (int w = f + q; w <= l; w += 16) {
-        const bool some = share_of(s.total, w + 1, n_workers) > share_of(s.total, w, n_workers);
-        ml[w - f][tid & 7] = some && row < s.n * a.G ? reinterpret_cast<const float2*>(record(w) + (size_t)rows * D)[row]
-                                                    : make_float2(-INFINITY, 0.0f);
-    }
-    __syncthreads();
-    if (row >= s.n * a.G) return;
-    float M = -INFINITY;
-    for (int w = 0; w <= l - f; ++w) M = fmaxf(M, ml[w][tid & 7].x);
+// worker c's range), if it is the first one inside its unit, and the unit's rows 8 y .. 8 y + 7. After
+// the segment's one round trip come the pieces' maxima and sums, then their outputs without waiting on
+// one another. Pieces are added in the order of the workers, 16 at a time. A small call waits for this
+// kernel's every instruction (cold code and one warp per scheduler: about 20 cycles each), so what can
+// be known before is left by the attention kernel.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedSeg* seg, const float* recs, T* O, float* lse, int rec_rows,
+                                                          int Hq, int G) {
+    __shared__ float2 ml[2][16][8];
+    const int tid = threadIdx.x, col = tid & 7, q = tid >> 3;
+    const PagedSeg s = seg[blockIdx.x + 1];
+    const int row = blockIdx.y * 8 + col;
+    if (blockIdx.y * 8 >= s.rows) return;
+    const bool in = row < s.rows;
     constexpr int C = D / 64;  // float4 columns per thread
-    float sum = 0.0f;
+    const size_t size = (size_t)rec_rows * (D + 2);  // of a record
+    const float* rec = recs + (size_t)s.first * 2 * size;  // the pieces' workers are neighbours
+    const size_t first = s.slot ? size : 0;
+    float M = -INFINITY, sum = 0.0f;
     float4 o[C];
 #pragma unroll
     for (int k = 0; k < C; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int w = 0; w <= l - f; ++w) {
-        const float2 x = ml[w][tid & 7];
-        if (x.x == -INFINITY && x.y == 0.0f) continue;
-        const float g = exp2f(x.x - M);  // (a piece of NaN scores alone has a sum and no maximum: NaN)
-        sum = fmaf(x.y, g, sum);
-        const float4* v = reinterpret_cast<const float4*>(record(f + w)) + row;
+    const int pieces = s.last - s.first + 1;
+    const float* mine = rec + (in ? row * 4 : 0) + (size_t)q * 4 * rec_rows;  // this thread's first float4
+    constexpr int N = 8;  // pieces in flight
+    float4 v[N][C];
+    auto fetch = [&](int p0) {
 #pragma unroll
-        for (int k = 0; k < C; ++k) {
-            const float4 y = v[(size_t)(q + 16 * k) * rows];
-            o[k].x = fmaf(y.x, g, o[k].x);
-            o[k].y = fmaf(y.y, g, o[k].y);
-            o[k].z = fmaf(y.z, g, o[k].z);
-            o[k].w = fmaf(y.w, g, o[k].w);
+        for (int i = 0; i < N; ++i) {
+            const int p = min(p0 + i, pieces - 1);
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                v[i][k] = *reinterpret_cast<const float4*>(mine + (size_t)p * 2 * size + (p ? 0 : first) + (size_t)(64 * k) * rec_rows);
+        }
+    };
+    for (int p0 = 0, turn = 0; p0 < pieces; p0 += 16, turn ^= 1) {
+        const int p = p0 + q;
+        float2 x = make_float2(-INFINITY, 0.0f);
+        if (in && p < pieces)
+            x = reinterpret_cast<const float2*>(rec + (size_t)p * 2 * size + (p ? 0 : first) + (size_t)rec_rows * D)[row];
+        fetch(p0);  // on their way with the maxima
+        ml[turn][q][col] = x;
+        __syncthreads();
+        float nm = M;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) nm = fmaxf(nm, ml[turn][i][col].x);
+        const float f0 = M == -INFINITY ? 0.0f : exp2_fast(M - nm);
+        M = nm;
+        sum *= f0;
+#pragma unroll
+        for (int k = 0; k < C; ++k) o[k] = make_float4(o[k].x * f0, o[k].y * f0, o[k].z * f0, o[k].w * f0);
+        const int n = min(16, pieces - p0);
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += N) {
+            if (i0 > 0) fetch(p0 + i0);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float2 y = ml[turn][i0 + i][col];
+                // (nothing seen, or no piece: neither maximum nor sum; NaN scores alone: a sum and no maximum)
+                const bool use = y.x != -INFINITY || y.y != 0.0f;
+                const float g = use ? exp2_fast(y.x - M) : 0.0f;
+                sum = fmaf(y.y, g, sum);
+#pragma unroll
+                for (int k = 0; k < C; ++k)
+                    if (use) {
+                        o[k].x = fmaf(v[i][k].x, g, o[k].x);
+                        o[k].y = fmaf(v[i][k].y, g, o[k].y);
+                        o[k].z = fmaf(v[i][k].z, g, o[k].z);
+                        o[k].w = fmaf(v[i][k].w, g, o[k].w);
+                    }
+            }
         }
     }
-    const int tok = row / a.G;
-    const size_t orow = (size_t)(s.row0 + tok) * a.Hq + s.head * a.G + row - tok * a.G;
+    if (!in) return;
+    const int tok = row / G;
+    const size_t orow = (size_t)(s.row0 + tok) * Hq + s.head * G + row - tok * G;
     const bool empty = s.pos0 + tok < 0;
     const float inv = 1.0f / sum;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-        T* out = static_cast<T*>(a.O) + orow * D + 4 * (q + 16 * k);
+        T* out = O + orow * D + 4 * (q + 16 * k);
         float v[4] = {o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv};
         if (empty) v[0] = v[1] = v[2] = v[3] = 0.0f;
         if constexpr (sizeof(T) == 2) {
@@ -359,26 +404,23 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedArgs a, int n_wor
             *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
         }
     }
-    if (a.lse && q == 0) a.lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+    if (lse && q == 0) lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
-// The merge after an attention grid of `workers` ranges whose units have at most `rows` rows, as its
-// programmatic dependent (its launch overlaps the grid's tail).
-template <typename T, int D, int KT>
+// The merge after an attention grid of `workers` ranges whose units have at most `rows` rows. (As a
+// programmatic dependent of that grid it measured 4 us slower per call: 24.0 against 19.5 us for one
+// token at 4k keys.) It asks for the attention grid's division of the SM's memory, so that an SM need
+// not change it between the two.
+template <typename T, int D>
 cudaError_t launch_paged_merge(const PagedArgs& a, int workers, int rows, cudaStream_t s) {
     if (workers < 2) return cudaSuccess;
-    if (workers > kMaxWorkers) return cudaErrorInvalidValue;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(workers - 1, (rows + 7) / 8);
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    const cudaError_t e = cudaFuncSetAttribute(paged_merge_kernel<T, D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                               cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
     count_launch();
-    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, KT>, a, workers);
+    paged_merge_kernel<T, D><<<dim3(workers - 1, (rows + 7) / 8), 128, 0, s>>>(a.seg, a.rec, static_cast<T*>(a.O), a.lse, a.rec_rows,
+                                                                               a.Hq, a.G);
+    return cudaGetLastError();
 }
 
 }  // namespace cobs

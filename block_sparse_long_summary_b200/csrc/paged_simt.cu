@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const float
     PagedWalk<kKT> w;
     int piece = 0;
     bool more = w.first(a, TQ, g);
-    if (tid == 0) a.seg[blockIdx.x] = w.seg(g);
+    if (tid == 0) a.seg[blockIdx.x] = w.seg(a, g, blockIdx.x);
     for (; more; more = w.next(a, TQ), ++piece) {
         const PagedEntry& e = w.e;
         const int rows = e.n * a.G, hi = e.last_pos();
@@ -217,7 +217,7 @@ cudaError_t run(const PagedArgs& a, int workers, const float* Q, long long q_str
     paged_simt_kernel<D, M><<<workers, kT, smem, s>>>(a, Q, q_stride, kc, vc);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_paged_merge<float, D, kKT>(a, workers, std::min(M / a.G, a.max_new) * a.G, s);
+    return launch_paged_merge<float, D>(a, workers, std::min(M / a.G, a.max_new) * a.G, s);
 }
 
 }  // namespace
