@@ -358,49 +358,54 @@ class PagedParams:
     dtype: str = "bf16"
     _structs: dict = dataclasses.field(default_factory=dict, init=False, compare=False, repr=False)
 
+    def __post_init__(self):
+        if self.dtype not in ("bf16", "f32"):
+            raise ValueError(f"dtype {self.dtype!r} (bf16 or f32)")
+        object.__setattr__(self, "torch_dtype", torch.bfloat16 if self.dtype == "bf16" else torch.float32)
+
     def c(self, q_stride: int = 0, kv_stride: int = 0) -> cobs_paged_params:
         cp = self._structs.get((q_stride, kv_stride))
         if cp is None:
-            if self.dtype not in ("bf16", "f32"):
-                raise ValueError(f"dtype {self.dtype!r} (bf16 or f32)")
             cp = cobs_paged_params(self.R, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages,
                                    self.n_tokens, self.max_new, self.window, self.sinks,
                                    COBS_BF16 if self.dtype == "bf16" else COBS_F32, q_stride, kv_stride)
             self._structs[q_stride, kv_stride] = cp
         return cp
 
-    @property
-    def torch_dtype(self):
-        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+
+# A serving step makes a few of these calls per layer, most of whose kernels run for microseconds, so the
+# checks are kept to one expression per tensor and the messages to a path of their own.
+
+def _refuse(t, name: str, dtype, numel: int, dev: int):
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must live on CUDA device {dev}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    raise ValueError(f"{name} must be contiguous with {numel} elements, got {tuple(t.shape)}")
 
 
 def _arg(t, name: str, dtype, numel: int, dev: int) -> int:
     """Address of a contiguous tensor of the given type and size on device `dev`."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must live on CUDA device {dev}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {numel} elements, got {tuple(t.shape)}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.numel() == numel and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, numel, dev)
 
 
 def _rows(t, name: str, p: PagedParams, heads: int, dev: int):
     """Address and token stride of [n_tokens, heads, d] rows (each token's heads contiguous)."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must live on CUDA device {dev}")
-    if t.dtype is not p.torch_dtype:
-        raise ValueError(f"{name} must be {p.torch_dtype}, not {t.dtype}")
-    if t.shape != (p.n_tokens, heads, p.d):
-        raise ValueError(f"{name} must be [{p.n_tokens}, {heads}, {p.d}], got {tuple(t.shape)}")
-    st = t.stride()
-    if p.n_tokens == 0:
+    n, d = p.n_tokens, p.d
+    if t.dtype is not p.torch_dtype or t.get_device() != dev or t.shape != (n, heads, d):
+        if t.dtype is p.torch_dtype and t.get_device() == dev:
+            raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
+        _refuse(t, name, p.torch_dtype, n * heads * d, dev)
+    if n == 0:
         return None, 0
-    if st[2] != 1 or (heads > 1 and st[1] != p.d):
+    st, dense = t.stride(), heads * d
+    if st[2] != 1 or (heads > 1 and st[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if p.n_tokens == 1 or st[0] == heads * p.d:
+    if n == 1 or st[0] == dense:
         return t.data_ptr(), 0
-    if st[0] < heads * p.d:
+    if st[0] < dense:
         raise ValueError(f"{name}: token rows overlap")
     return t.data_ptr(), st[0]
 
@@ -411,14 +416,19 @@ def _device_of(t) -> int:
     return t.get_device()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(dev: int, stream, fn, *args):
     """Enqueue on `stream` (default: the current one of the tensors' device), that device current."""
-    raw = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream.cuda_stream
+    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        _check(fn(*args, raw))
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, raw))
+            status = fn(*args, raw)
+    if status != COBS_OK:
+        _check(status)
 
 
 def paged_workspace_bytes(p: PagedParams) -> int:

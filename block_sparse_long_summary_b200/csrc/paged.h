@@ -5,9 +5,26 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/cobs.h"
 
 namespace cobs {
+
+// Whether a kernel's attributes (one flag array per kernel) have still to be set on the current device.
+// Setting them twice, by two threads at once, does no harm.
+struct OncePerDevice {
+    std::atomic<bool> done[64] = {};
+    template <typename F> cudaError_t run(F&& set) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+        e = set();
+        if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
+        return e;
+    }
+};
 
 constexpr int kMaxRequests = 16384;  // the kernels keep one int per request in shared memory
 

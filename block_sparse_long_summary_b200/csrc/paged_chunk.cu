@@ -736,7 +736,8 @@ cudaError_t run(const PagedDims& m, const PagedArgs& a, const void* Q, const voi
     if (!encode_tmap_bf16_3d(&maps.q, Q, qd, qs, qb) || !encode_tmap_bf16_3d(&maps.k, kc, cd, cs, cb) ||
         !encode_tmap_bf16_3d(&maps.v, vc, cd, cs, cb))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    static OncePerDevice once;
+    cudaError_t e = once.run([] { return cudaFuncSetAttribute(paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem); });
     if (e != cudaSuccess) return e;
     count_launch();
     paged_chunk_kernel<D><<<workers, kThreads, C::kSmem, s>>>(maps, a);

@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "dims.h"
+#include "paged.h"
 
 namespace cobs {
 
@@ -418,8 +419,10 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedSeg* seg, c
 template <typename T, int D>
 cudaError_t launch_paged_merge(const PagedArgs& a, int workers, int rows, cudaStream_t s) {
     if (workers < 2) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(paged_merge_kernel<T, D>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                               cudaSharedmemCarveoutMaxShared);
+    static OncePerDevice once;
+    const cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(paged_merge_kernel<T, D>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    });
     if (e != cudaSuccess) return e;
     count_launch();
     paged_merge_kernel<T, D><<<dim3(workers - 1, (rows + 7) / 8), 128, 0, s>>>(a.seg, a.rec, static_cast<T*>(a.O), a.lse, a.rec_rows,
