@@ -10,6 +10,7 @@
 // this one run, V of this tile while its scores are formed. The float32 products stay on the FMA
 // pipes: the tensor cores' tf32 would drop 13 bits of each factor.
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.h"
 #include "paged_plan.cuh"
@@ -35,8 +36,12 @@ constexpr size_t simt_smem() {
     return sizeof(float) * ((size_t)M * (D + 4) + (size_t)kKT * (D + 4) + (size_t)kKT * D + (size_t)M * kPS);
 }
 
+// Blocks resident on an SM (shared memory and registers): one waits for its copies and its barriers, the
+// others compute.
+constexpr int blocks_per_sm(int d, int m) { return m == 16 ? (d == 64 ? 3 : 2) : (d == 64 ? 2 : 1); }
+
 template <int D, int M>
-__global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const float* Q, long long q_stride,
+__global__ void __launch_bounds__(kT, blocks_per_sm(D, M)) paged_simt_kernel(PagedArgs a, const float* Q, long long q_stride,
                                                         const float* kc, const float* vc) {
     extern __shared__ __align__(16) float sm[];
     __shared__ long long tmp[2 * kT / 32];
@@ -138,12 +143,12 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const float
 #pragma unroll
                 for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
                 const float nm = fmaxf(m[y], mx), use = nm == -INFINITY ? 0.0f : nm;
-                const float f = m[y] == nm ? 1.0f : exp2f(m[y] - use);
+                const float f = m[y] == nm ? 1.0f : exp2_fast(m[y] - use);
                 m[y] = nm;
                 float sum = 0.0f;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float pv = exp2f(s[y][x] - use);
+                    const float pv = exp2_fast(s[y][x] - use);
                     sP[(ty + 16 * y) * kPS + tx + 16 * x] = pv;
                     sum += pv;
                 }
@@ -153,28 +158,32 @@ __global__ void __launch_bounds__(kT) paged_simt_kernel(PagedArgs a, const float
             }
             cp_wait<1>();  // V
             __syncthreads();
+            // a hidden key adds nothing, whatever its value holds: tiles with masks test every pair (the test
+            // costs as much as the products, so the others do without)
+            auto product = [&](auto masked) {
 #pragma unroll 2
-            for (int j = 0; j < kKT; j += 4) {
-                float4 p4[RM];
+                for (int j = 0; j < kKT; j += 4) {
+                    float4 p4[RM];
 #pragma unroll
-                for (int y = 0; y < RM; ++y) p4[y] = *reinterpret_cast<const float4*>(sP + (ty + 16 * y) * kPS + j);
+                    for (int y = 0; y < RM; ++y) p4[y] = *reinterpret_cast<const float4*>(sP + (ty + 16 * y) * kPS + j);
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    float v[CD];
+                    for (int jj = 0; jj < 4; ++jj) {
+                        float v[CD];
 #pragma unroll
-                    for (int x = 0; x < CD; x += 4)
-                        *reinterpret_cast<float4*>(v + x) =
-                            *reinterpret_cast<const float4*>(sV + (j + jj) * D + (x / 4) * 64 + tx * 4);
+                        for (int x = 0; x < CD; x += 4)
+                            *reinterpret_cast<float4*>(v + x) =
+                                *reinterpret_cast<const float4*>(sV + (j + jj) * D + (x / 4) * 64 + tx * 4);
 #pragma unroll
-                    for (int y = 0; y < RM; ++y) {
-                        const float pv = jj == 0 ? p4[y].x : jj == 1 ? p4[y].y : jj == 2 ? p4[y].z : p4[y].w;
-                        // a hidden key adds nothing, whatever its value holds
-                        const bool use = full || visible(j0 + j + jj, pos[y], a.W, a.S);
+                        for (int y = 0; y < RM; ++y) {
+                            const float pv = jj == 0 ? p4[y].x : jj == 1 ? p4[y].y : jj == 2 ? p4[y].z : p4[y].w;
+                            if (!decltype(masked)::value || visible(j0 + j + jj, pos[y], a.W, a.S))
 #pragma unroll
-                        for (int x = 0; x < CD; ++x) o[y][x] = use ? fmaf(pv, v[x], o[y][x]) : o[y][x];
+                                for (int x = 0; x < CD; ++x) o[y][x] = fmaf(pv, v[x], o[y][x]);
+                        }
                     }
                 }
-            }
+            };
+            if (full) product(std::false_type()); else product(std::true_type());
             __syncthreads();  // V and P have been read
         }
         const bool whole = w.whole();
@@ -226,7 +235,7 @@ cudaError_t run(const PagedArgs& a, int workers, const float* Q, long long q_str
 static int simt_rows(const PagedDims& m) { return (long long)m.max_new * m.G <= 16 ? 16 : 64; }
 
 int paged_simt_rec_rows(const PagedDims& m) { return simt_rows(m); }
-int paged_simt_workers(const PagedDims& m) { return sm_count() * (simt_rows(m) == 16 ? 2 : 1); }
+int paged_simt_workers(const PagedDims& m) { return sm_count() * blocks_per_sm(m.d, simt_rows(m)); }
 
 cudaError_t launch_paged_simt(const PagedDims& m, const PagedArgs& a, const float* Q, const float* kc,
                               const float* vc, cudaStream_t s) {
