@@ -7,7 +7,8 @@
 // rows are two MMA tiles of 128: each holds floor(128 / G) tokens x the G heads of the group, so K
 // and V are read once per group and a tile spans few positions. Per key tile and row tile g:
 //   S_g = Q_g K^T           tcgen05.mma, M 128, N 128, K d, into 128 TMEM columns
-//   p = 2^(s c - m)         one thread per row: the row in registers, no exchange between threads;
+//   p = 2^(s c - m)         two threads per row (a warp alone on its scheduler waits for its own
+//                           instructions: with one thread per row a pair of tiles took 4.2k cycles, now X);
 //                           m moves only when a row's maximum grows by more than 2^8 (then the
 //                           thread rescales its row of O, which is seldom)
 //   O_g += P_g V            P in bf16 over S's columns (A operand from TMEM), V MN-major
@@ -17,9 +18,9 @@
 // O_g is up to date, and no barrier is needed for either. A unit of one row tile (single tokens,
 // short chunks) gives both halves of the machine to it: the two groups take its key tiles in turn,
 // each with an accumulator and maxima of its own, joined at the unit's end.
-// Roles: warps 0-3 and 4-7 softmax and epilogue of row tiles 0 and 1; warp 8 loads (one TMA box per
-// page and 64 columns; pages no row needs come as out-of-range boxes, that is zeros); warp 9 issues
-// the MMAs; warps 10 and 11 (the first also loads Q) prepare V of the tiles that some row does not see in full: rows of V no
+// Roles: warps 0-15 softmax and epilogue (four for each row tile and half of the columns); warp 16 loads (one TMA box per
+// page and 64 columns; pages no row needs come as out-of-range boxes, that is zeros); warp 17 issues
+// the MMAs; warps 18 and 19 (the first also loads Q) prepare V of the tiles that some row does not see in full: rows of V no
 // row of the unit sees (slots behind the keys, keys before the window: any bits) are set to zero,
 // since 0 * NaN would reach O, and the others are looked over for infinities and NaN: such a tile's
 // product is formed by the softmax threads, key by key, so that only the rows that see them change.
@@ -35,19 +36,30 @@
 namespace cobs {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kKT = 128;      // keys per tile
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kFixWarp = 10;
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kFixWarp = 18;
 constexpr int kFixDepth = 4;    // tiles whose V may be prepared ahead of their products
 constexpr uint32_t kBox = 128 * 128;  // 128 rows of 64 columns
 constexpr uint32_t kColO = 256;       // S_g (and P_g) at 128 g, O_g at 256 + 128 g
+
+// Shared memory behind Q and the ring.
+template <int STAGES>
+struct Misc {
+    uint64_t barQ, barQfree, barKV[STAGES], barFree[STAGES], barS[2], barP[2], barO[2], barFix[kFixDepth], barDone;
+    long long tmp[2 * kThreads / 32];
+    PagedRange range;
+    int dirty[kFixDepth][2];
+    uint32_t tmem;
+    float row[2][2][128];  // [group][half of the columns][row]: maxima of a tile, sums and maxima of a unit
+};
 
 template <int D>
 struct Cfg {
     static constexpr int H = D / 64;                  // 64-column halves
     static constexpr uint32_t kTile = H * kBox;       // a row tile of Q, a key tile of K or V
     static constexpr int kStages = D == 128 ? 5 : 8;  // K and V tiles in flight
-    static constexpr uint32_t kSmem = 1024 + (2 + kStages) * kTile;
+    static constexpr uint32_t kSmem = (2 + kStages) * kTile + sizeof(Misc<kStages>);
     static constexpr uint32_t kIdescS = tc::idesc_bf16(128, kKT, 0, 0);
     static constexpr uint32_t kIdescPV = tc::idesc_bf16(128, D, 0, 1);
 };
@@ -93,8 +105,6 @@ __device__ __forceinline__ float ld1(uint32_t taddr) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr));
     return v;
 }
-// The two warps (one of each group) that hold the same rows.
-__device__ __forceinline__ void pair_sync(int w) { asm volatile("bar.sync %0, 64;" ::"r"(1 + w) : "memory"); }
 template <int N> __device__ __forceinline__ void rows_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
 // shared memory to global, both 16-byte aligned, a multiple of 16 bytes
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
@@ -187,20 +197,26 @@ __device__ __forceinline__ bool masked_tile(const PagedArgs& a, const PagedEntry
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, PagedArgs a) {
     using C = Cfg<D>;
-    extern __shared__ unsigned char smem_raw[];
-    __shared__ __align__(8) uint64_t barQ, barQfree, barKV[C::kStages], barFree[C::kStages], barS[2], barP[2], barO[2], barFix[kFixDepth], barDone;
-    __shared__ uint32_t tmem_sh;
-    __shared__ int dirty_sh[kFixDepth][2];
-    __shared__ long long tmp[2 * kThreads / 32];
-    __shared__ PagedRange range;
-    __shared__ float2 ml_sh[128];  // a pair's maxima and sums
-    unsigned char* sQ = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) unsigned char sQ[];  // (no other shared memory: it starts at its first kilobyte)
     unsigned char* sKV = sQ + 2 * C::kTile;
-
+    Misc<C::kStages>& sh_ = *reinterpret_cast<Misc<C::kStages>*>(sKV + C::kStages * C::kTile);
+    uint64_t &barQ = sh_.barQ, &barQfree = sh_.barQfree, &barDone = sh_.barDone;
+    auto& barKV = sh_.barKV;
+    auto& barFree = sh_.barFree;
+    auto& barS = sh_.barS;
+    auto& barP = sh_.barP;
+    auto& barO = sh_.barO;
+    auto& barFix = sh_.barFix;
+    auto& dirty_sh = sh_.dirty;
+    auto& row_sh = sh_.row;
+    if (smem_addr(sQ) & 1023u) {  // the swizzled tiles need it
+        report_error(a.err, kErrWaitTimeout);
+        return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int TM = 128 / a.G, TQ = 2 * TM;  // tokens of a row tile and of a unit
     if (warp == 0) {
-        tc::tmem_alloc(&tmem_sh, 512);
+        tc::tmem_alloc(&sh_.tmem, 512);
         tc::tmem_relinquish();
     }
     if (tid == 32) {
@@ -212,29 +228,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&barS[g], 1);
-            mbar_init(&barP[g], 4);
+            mbar_init(&barP[g], 8);
             mbar_init(&barO[g], 1);
         }
         for (int f = 0; f < kFixDepth; ++f) mbar_init(&barFix[f], 2);
         mbar_init(&barDone, 1);
         fence_barrier_init();
     }
-    plan_range<kThreads, kKT>(a, TQ, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sKV), tmp, &range);
+    plan_range<kThreads, kKT>(a, TQ, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sKV), sh_.tmp, &sh_.range);
     fence_proxy_async();  // the plan's use of the ring before TMA's
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const PagedRange rg = range;
-    const uint32_t tmem = tmem_sh;
+    const PagedRange rg = sh_.range;
+    const uint32_t tmem = sh_.tmem;
     bool ok = true;
     PagedWalk<kKT> w;
     bool more = w.first(a, TQ, rg);
     if (tid == kFixWarp * 32 + 32) a.seg[blockIdx.x] = w.seg(a, rg, blockIdx.x);
 
-    if (warp < 8) {
+    if (warp < 16) {
         // ------------------------------------------------------------ softmax and epilogue of row tile g
         // (after a wait that gave up these warps go on without waiting: they meet at named barriers)
-        const int g = warp >> 2, row = tid & 127;
+        const int g = (warp >> 2) & 1, half = warp >> 3, row = tid & 127;  // row tile, half of the columns
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + 128 * g, tO = tmem + lanes + kColO + 128 * g;
         const int tok = row / a.G, hrow = row - tok * a.G;
@@ -269,9 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 tc::fence_after_sync();
                 if (warp_live) {
                     const int hi = t - j0, lo = a.W > 0 ? hi - a.W + 1 : 0, sk = a.W > 0 ? a.S - j0 : 0;
+                    const uint32_t tH = tS + 64 * half;
                     if (masked) {  // the scores this row does not see: -infinity, in place
 #pragma unroll 1
-                        for (int c = 0; c < kKT; c += 32) {
+                        for (int c = 64 * half; c < 64 * half + 64; c += 32) {
                             const uint32_t see = bits_below(hi - c + 1) & (~bits_below(lo - c) | bits_below(sk - c));
                             float s[32];
                             ld32_to(tS + c, s);
@@ -282,27 +299,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                         }
                         tc::wait_st();
                     }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int c = 0; c < kKT; c += 64) {
-                        float s[32], s1[32];
-                        ld32_to(tS + c, s);
-                        ld32_to(tS + c + 32, s1);
-                        wait_ld32(s);
-                        touch32(s1);
+                    float mx[2] = {-INFINITY, -INFINITY};
+                    float s[32];
+                    ld32_to(tH, s);
+                    wait_ld32(s);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            mx[j & 2] = max3(mx[j & 2], s[j], s[j + 1]);
-                            mx[(j & 2) + 1] = max3(mx[(j & 2) + 1], s1[j], s1[j + 1]);
-                        }
-                    }
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                    for (int j = 0; j < 32; j += 2) mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], s[j], s[j + 1]);
+                    ld32_to(tH + 32, s);
+                    wait_ld32(s);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], s[j], s[j + 1]);
+                    const float mine = fmaxf(mx[0], mx[1]);
+                    row_sh[g][half][row] = mine;
+                    rows_sync<64>(1 + 4 * g + (warp & 3));  // the warp with the other half of these rows
+                    const float mt = fmaxf(mine, row_sh[g][half ^ 1][row]) * sl2;
                     const bool grow = mt > m + 8.0f;  // (from -infinity too; never for a row that sees nothing)
                     if (k > kg && __any_sync(kFull, grow && m != -INFINITY)) {
                         const float f = grow ? tc::ex2(m - mt) : 1.0f;
                         l *= f;
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
+                        for (int c = half * (D / 2); c < half * (D / 2) + D / 2; c += 32) {
                             float o[32];
                             ld32_to(tO + c, o);
                             wait_ld32(o);
@@ -314,13 +330,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     }
                     if (grow) m = mt;
                     const float neg = m == -INFINITY ? 0.0f : -m;
-                    // p = 2^(s c - m) of 32 keys at a time, the next ones on their way from TMEM: P, half as
-                    // wide, follows behind the scores still to be read. The loops stay rolled: unrolled over
-                    // the 128 keys the code outgrew the instruction caches and every pass waited for it.
+                    // p = 2^(s c - m) of 32 keys at a time; P, half as wide, over this half's own scores
                     float2 ps[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     const float2 scale = make_float2(sl2, sl2), shift = make_float2(neg, neg);
-                    auto powers = [&](const float (&s)[32], int c) {
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
                         uint32_t pk[16];
+                        ld32_to(tH + c, s);
+                        wait_ld32(s);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             float2 x = fma2(make_float2(s[2 * j], s[2 * j + 1]), scale, shift);
@@ -329,20 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                             ps[j & 1] = add2(ps[j & 1], x);
                             pk[j] = pack_bf16(x.x, x.y);
                         }
-                        if (!dirty) st16(tS + c / 2, pk);
-                    };
-                    {
-                        float s[32], s1[32];
-                        ld32_to(tS, s);
-#pragma unroll 1
-                        for (int c = 0; c < kKT; c += 64) {
-                            wait_ld32(s);
-                            ld32_to(tS + c + 32, s1);
-                            powers(s, c);
-                            wait_ld32(s1);
-                            if (c + 64 < kKT) ld32_to(tS + c + 64, s);
-                            powers(s1, c + 32);
-                        }
+                        if (!dirty) st16(tH + c / 2, pk);
                     }
                     ps[0] = add2(ps[0], ps[1]);
                     l += ps[0].x + ps[0].y;
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                         // tensor cores take it, V from the ring
                         const unsigned char* sV = sKV + (size_t)(dirty - 1) * C::kTile;
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
+                        for (int c = half * (D / 2); c < half * (D / 2) + D / 2; c += 32) {
                             float o[32];
                             if (k > kg) {
                                 ld32_to(tO + c, o);
@@ -400,28 +404,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             at.advance(sh.stages);
             if (ok && sh.staged) ok = wait_on(&barKV[mine.s], mine.ph, a.err);
             tc::fence_after_sync();
-            // A pair's threads of one row are in warps of the same TMEM lanes: each joins half of the columns
-            // of both accumulators.
-            float f0 = 1.0f, f1 = 0.0f;  // factors of O_0 and O_1 (of O_g alone, if not a pair)
+            // The threads of one row are in warps of the same TMEM lanes: two of each group, each with a share
+            // of the columns, of both accumulators if the unit's tiles went to both groups.
+            float f0 = 1.0f, f1 = 0.0f;  // factors of O_0 and O_1 (of O_g alone, if not both)
             const bool both = pair && w.t1 - w.t0 > 1, empty = t < 0, whole = w.whole();
-            if (warp_live) {
+            if (warp_live && any) {
+                auto meet = [&] { if (both) rows_sync<128>(9 + (warp & 3)); else rows_sync<64>(1 + 4 * g + (warp & 3)); };
+                row_sh[g][half][row] = l;
+                meet();
+                l = row_sh[g][0][row] + row_sh[g][1][row];
                 if (both) {
-                    float2 x = make_float2(m, l), y = x;  // group 0's and group 1's, exchanged through one slot
-                    if (g == 1) ml_sh[row] = y;
-                    pair_sync(warp & 3);
-                    if (g == 0) {
-                        y = ml_sh[row];
-                        ml_sh[row] = x;
-                    }
-                    pair_sync(warp & 3);
-                    if (g == 1) x = ml_sh[row];
-                    m = fmaxf(x.x, y.x);
+                    const float l0 = row_sh[0][0][row] + row_sh[0][1][row], l1 = row_sh[1][0][row] + row_sh[1][1][row];
+                    meet();
+                    row_sh[g][half][row] = m;
+                    meet();
+                    const float m0 = row_sh[0][0][row], m1 = row_sh[1][0][row];
+                    m = fmaxf(m0, m1);
                     // (a group of NaN scores alone has a sum and no maximum: NaN then)
-                    f0 = x.x == -INFINITY && x.y == 0.0f ? 0.0f : tc::ex2(x.x - m);
-                    f1 = y.x == -INFINITY && y.y == 0.0f ? 0.0f : tc::ex2(y.x - m);
-                    l = x.y * f0 + y.y * f1;
+                    f0 = m0 == -INFINITY && l0 == 0.0f ? 0.0f : tc::ex2(m0 - m);
+                    f1 = m1 == -INFINITY && l1 == 0.0f ? 0.0f : tc::ex2(m1 - m);
+                    l = l0 * f0 + l1 * f1;
                 }
-                const int c0 = both ? g * (D / 2) : 0, c1 = both ? c0 + D / 2 : D;
+                meet();  // before the slots are written again
+                const int c0 = both ? 32 * (2 * g + half) : half * (D / 2), c1 = both ? min(c0 + 32, D) : c0 + D / 2;
                 const size_t orow = (size_t)(e.row0 + tok0 + (live ? tok : 0)) * a.Hq + w.h * a.G + (live ? hrow : 0);
                 float* rec = a.rec + ((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * a.rec_rows * (D + 2);
                 const int rrow = live ? (tok0 + tok) * a.G + hrow : 0;
@@ -431,20 +436,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     f0 = empty ? 0.0f : f0 / l;
                     f1 = empty ? 0.0f : f1 / l;
                 }
-                if (any) {
+                {
 #pragma unroll 1
                     for (int c = c0; c < c1; c += 32) {
                         float o[32];
                         ld32_to((both ? tmem + lanes + kColO : tO) + c, o);
                         wait_ld32(o);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = f0 != 0.0f ? o[j] * f0 : 0.0f;
+                        for (int j = 0; j < 32; ++j) o[j] *= f0;  // (a row that sees nothing: 0 * 0)
                         if (both) {
                             float o1[32];
                             ld32_to(tmem + lanes + kColO + 128 + c, o1);
                             wait_ld32(o1);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = f1 != 0.0f ? fmaf(o1[j], f1, o[j]) : o[j];
+                            for (int j = 0; j < 32; ++j) o[j] = fmaf(o1[j], f1, o[j]);
                         }
                         if (whole) {
                             uint4 v[4];
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                         }
                     }
                 }
-                if (live && any && (!both || g == 0)) {
+                if (live && half == 0 && (!both || g == 0)) {
                     if (!whole) {
                         reinterpret_cast<float2*>(rec + (size_t)a.rec_rows * D)[rrow] = make_float2(m, l);
                     } else if (a.lse) {
@@ -487,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             tc::fence_before_sync();
             if (sh.staged) {
                 fence_proxy_async();
-                if (pair) rows_sync<256>(5); else rows_sync<128>(5 + g);
-                if ((warp & 3) == 0 && (!pair || g == 0)) {  // a token's rows of the group are one run of both memories
+                if (pair) rows_sync<512>(15); else rows_sync<256>(13 + g);
+                if ((warp & 3) == 0 && half == 0 && (!pair || g == 0)) {  // a token's rows of the group are one run of both memories
                     const unsigned char* src = sKV + (size_t)mine.s * C::kTile;
                     for (int i = lane; i < ntok; i += 32)
                         bulk_s2g(static_cast<__nv_bfloat16*>(a.O) + ((size_t)(e.row0 + tok0 + i) * a.Hq + w.h * a.G) * D,
@@ -499,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     if (lane == 0) mbar_arrive(&barFree[mine.s]);
                 }
             } else if (both && warp_live) {
-                pair_sync(warp & 3);
+                rows_sync<128>(9 + (warp & 3));
             }
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     const uint64_t vb = desc_v + kv_addr + i.s * (C::kTile >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kKT / 16; ++kk)
-                        mma_f16_ts(tmem + kColO + 128 * g, tmem + 128 * g + 8 * kk, vb + kk * (16 * 128 >> 4), C::kIdescPV, add || kk > 0);
+                        mma_f16_ts(tmem + kColO + 128 * g, tmem + 128 * g + 64 * (kk >> 2) + 8 * (kk & 3), vb + kk * (16 * 128 >> 4), C::kIdescPV, add || kk > 0);
                 };
                 for (; more && ok; more = w.next(a, TQ), ++u) {
                     const PagedEntry& e = w.e;
