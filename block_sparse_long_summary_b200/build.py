@@ -1,8 +1,10 @@
-"""Build the COBS CUDA library (``lib/libcobs.so``) for sm_100a with nvcc.
+"""Build the COBS CUDA library (``lib/libcobs.so``) for sm_100a with nvcc, and the native binding of its
+paged-cache calls (``lib/_paged.so``) with the host compiler.
 
 Usage: ``python -m block_sparse_long_summary_b200.build [--force]``.
 The library is built in place (objects under ``_build/``) so that it travels with the
-source tree; it links the CUDA runtime statically and nothing from PyTorch.
+source tree; it links the CUDA runtime statically and nothing from PyTorch. The binding links the
+library and PyTorch.
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libcobs.so")
+BINDING = os.path.join(LIB_DIR, "_paged.so")
+BINDING_SRC = "paged_binding.cpp"
 SOURCES = ["api.cu", "summary.cu", "select.cu", "decode.cu", "decode_stream.cu", "decode_step.cu", "tma.cu", "prefill.cu",
            "mass.cu", "basis.cu", "paged_tables.cu", "paged_attn.cu", "paged_simt.cu",
            "paged_chunk.cu"]
@@ -37,7 +41,7 @@ def nvcc() -> str:
 
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS if os.path.exists(os.path.join(CSRC, s))]
-    files.append(os.path.join(ROOT, "include", "cobs.h"))
+    files += [os.path.join(ROOT, "include", "cobs.h"), os.path.join(CSRC, BINDING_SRC)]
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 
@@ -55,8 +59,28 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    """The binding of the paged calls: it finds the library beside itself and PyTorch's libraries in the
+    process that imports it."""
+    import sysconfig
+
+    from torch.utils import cpp_extension as ext
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-w", os.path.join(CSRC, BINDING_SRC), "-o", tmp,
+           "-I", sysconfig.get_paths()["include"], "-I", cuda, *[a for d in ext.include_paths() for a in ("-isystem", d)],
+           "-L", LIB_DIR, "-lcobs", "-Wl,-rpath,$ORIGIN", *[a for d in ext.library_paths() for a in ("-L", d)],
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    import torch
+    cmd.append(f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the paged binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, BINDING)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
@@ -69,6 +93,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_binding()
     return LIB
 
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import importlib.util
 import os
 
 import torch
@@ -356,79 +357,37 @@ class PagedParams:
     window: int = 0
     sinks: int = 0
     dtype: str = "bf16"
-    _structs: dict = dataclasses.field(default_factory=dict, init=False, compare=False, repr=False)
 
     def __post_init__(self):
         if self.dtype not in ("bf16", "f32"):
             raise ValueError(f"dtype {self.dtype!r} (bf16 or f32)")
-        object.__setattr__(self, "torch_dtype", torch.bfloat16 if self.dtype == "bf16" else torch.float32)
+        cp = cobs_paged_params(self.R, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages, self.n_tokens,
+                               self.max_new, self.window, self.sinks, COBS_BF16 if self.dtype == "bf16" else COBS_F32, 0, 0)
+        object.__setattr__(self, "_struct", cp)
+        object.__setattr__(self, "address", ctypes.addressof(cp))
 
     def c(self, q_stride: int = 0, kv_stride: int = 0) -> cobs_paged_params:
-        cp = self._structs.get((q_stride, kv_stride))
-        if cp is None:
-            cp = cobs_paged_params(self.R, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages,
-                                   self.n_tokens, self.max_new, self.window, self.sinks,
-                                   COBS_BF16 if self.dtype == "bf16" else COBS_F32, q_stride, kv_stride)
-            self._structs[q_stride, kv_stride] = cp
+        """The C struct (a copy), with dense token rows unless told otherwise."""
+        cp = cobs_paged_params.from_buffer_copy(self._struct)
+        cp.q_stride, cp.kv_stride = q_stride, kv_stride
         return cp
 
-
-# A serving step makes a few of these calls per layer, most of whose kernels run for microseconds, so the
-# checks are kept to one expression per tensor and the messages to a path of their own.
-
-def _refuse(t, name: str, dtype, numel: int, dev: int):
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name} must live on CUDA device {dev}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    raise ValueError(f"{name} must be contiguous with {numel} elements, got {tuple(t.shape)}")
+    @property
+    def torch_dtype(self):
+        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
 
 
-def _arg(t, name: str, dtype, numel: int, dev: int) -> int:
-    """Address of a contiguous tensor of the given type and size on device `dev`."""
-    if t.dtype is dtype and t.numel() == numel and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, name, dtype, numel, dev)
+def _load_binding(path: str = os.path.join(_HERE, "lib", "_paged.so")):
+    if not os.path.exists(path):
+        raise ImportError(f"binding of the paged calls not built: {path} is missing "
+                          "(run python -m block_sparse_long_summary_b200.build)")
+    spec = importlib.util.spec_from_file_location("_paged", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
-def _rows(t, name: str, p: PagedParams, heads: int, dev: int):
-    """Address and token stride of [n_tokens, heads, d] rows (each token's heads contiguous)."""
-    n, d = p.n_tokens, p.d
-    if t.dtype is not p.torch_dtype or t.get_device() != dev or t.shape != (n, heads, d):
-        if t.dtype is p.torch_dtype and t.get_device() == dev:
-            raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {tuple(t.shape)}")
-        _refuse(t, name, p.torch_dtype, n * heads * d, dev)
-    if n == 0:
-        return None, 0
-    st, dense = t.stride(), heads * d
-    if st[2] != 1 or (heads > 1 and st[1] != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if n == 1 or st[0] == dense:
-        return t.data_ptr(), 0
-    if st[0] < dense:
-        raise ValueError(f"{name}: token rows overlap")
-    return t.data_ptr(), st[0]
-
-
-def _device_of(t) -> int:
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
-    return t.get_device()
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _call(dev: int, stream, fn, *args):
-    """Enqueue on `stream` (default: the current one of the tensors' device), that device current."""
-    raw = _raw_stream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status != COBS_OK:
-        _check(status)
+_paged = _load_binding()
 
 
 def paged_workspace_bytes(p: PagedParams) -> int:
@@ -445,42 +404,30 @@ def alloc_paged_workspace(p: PagedParams, device="cuda") -> torch.Tensor:
         return torch.empty(n, dtype=torch.uint8, device=dev)
 
 
+# Tensors are checked (device, type, shape, strides) and passed on by the native binding, on `stream` or
+# the current stream of their device, with that device current.
+
 def cobs_paged_tables(p: PagedParams, cached_len, new_len, free_pages, free_count, block_table, cu_new, kv_len, slot_map,
                       counts, stream=None):
     """Block-table entries of the pages that the new tokens open, slot map and running sums, from the lengths."""
-    dev, i32 = _device_of(cached_len), torch.int32
-    _call(dev, stream, _lib.cobs_paged_tables, ctypes.byref(p.c()), _arg(cached_len, "cached_len", i32, p.R, dev),
-          _arg(new_len, "new_len", i32, p.R, dev), _arg(free_pages, "free_pages", i32, free_pages.numel(), dev) or None,
-          free_pages.numel(), _arg(free_count, "free_count", i32, 1, dev),
-          _arg(block_table, "block_table", i32, p.R * p.max_pages, dev), _arg(cu_new, "cu_new", i32, p.R + 1, dev),
-          _arg(kv_len, "kv_len", i32, p.R, dev), _arg(slot_map, "slot_map", i32, p.n_tokens, dev) or None,
-          _arg(counts, "counts", i32, 4, dev))
+    status = _paged.tables(p.address, cached_len, new_len, free_pages, free_count, block_table, cu_new, kv_len, slot_map,
+                           counts, stream)
+    if status:
+        _check(status)
 
 
 def cobs_paged_append(p: PagedParams, K, V, slot_map, k_cache, v_cache, stream=None):
     """Copy the new K and V rows to the slots of the caches."""
-    dev = _device_of(k_cache)
-    k, ks = _rows(K, "K", p, p.Hkv, dev)
-    v, vs = _rows(V, "V", p, p.Hkv, dev)
-    if ks != vs:
-        raise ValueError("K and V must have the same token stride")
-    n = p.n_pages * p.Hkv * p.page * p.d
-    _call(dev, stream, _lib.cobs_paged_append, ctypes.byref(p.c(0, ks)), k, v,
-          _arg(slot_map, "slot_map", torch.int32, p.n_tokens, dev) or None, _arg(k_cache, "k_cache", p.torch_dtype, n, dev),
-          _arg(v_cache, "v_cache", p.torch_dtype, n, dev))
+    status = _paged.append(p.address, K, V, slot_map, k_cache, v_cache, stream)
+    if status:
+        _check(status)
 
 
 def cobs_paged_attn(p: PagedParams, Q, k_cache, v_cache, block_table, cu_new, kv_len, O, lse, workspace, stream=None):
     """Attention of every request's new tokens over its pages (lse: [n_tokens, Hq] float32, or None)."""
-    dev, i32 = _device_of(k_cache), torch.int32
-    q, qs = _rows(Q, "Q", p, p.Hq, dev)
-    n = p.n_pages * p.Hkv * p.page * p.d
-    _call(dev, stream, _lib.cobs_paged_attn, ctypes.byref(p.c(qs)), q, _arg(k_cache, "k_cache", p.torch_dtype, n, dev),
-          _arg(v_cache, "v_cache", p.torch_dtype, n, dev), _arg(block_table, "block_table", i32, p.R * p.max_pages, dev),
-          _arg(cu_new, "cu_new", i32, p.R + 1, dev), _arg(kv_len, "kv_len", i32, p.R, dev),
-          _arg(O, "O", p.torch_dtype, p.n_tokens * p.Hq * p.d, dev) or None,
-          None if lse is None else _arg(lse, "lse", torch.float32, p.n_tokens * p.Hq, dev) or None,
-          _arg(workspace, "workspace", torch.uint8, workspace.numel(), dev), workspace.numel())
+    status = _paged.attn(p.address, Q, k_cache, v_cache, block_table, cu_new, kv_len, O, lse, workspace, stream)
+    if status:
+        _check(status)
 
 
 @dataclasses.dataclass

@@ -354,6 +354,39 @@ def test_side_stream_and_no_lse():
     assert (b.lse == 7).all()
 
 
+def test_binding_checks_tensors():
+    C = cobs()
+    b = Batch(C, [(30, 4), (5, 1)], 4, 2, 64, 16, junk=0.0)
+    p = b.p
+    wide = torch.zeros((p.n_tokens, 8, 64), dtype=torch.bfloat16, device="cuda")
+
+    def attn(**kw):
+        t = dict(Q=b.Q, k_cache=b.k_cache, v_cache=b.v_cache, block_table=b.table, cu_new=b.cu, kv_len=b.kv_len, O=b.O, lse=None,
+                 workspace=b.ws)
+        t.update(kw)
+        C.cobs_paged_attn(p, *t.values())
+
+    attn()
+    attn(Q=wide[:, :4])
+    for bad, why in ((dict(Q=wide[:, ::2]), "contiguous"), (dict(Q=wide[:-1, :4]), "must be"), (dict(Q=b.Q.float()), "bfloat16"),
+                     (dict(Q=wide[:1, :4].expand(p.n_tokens, 4, 64)), "overlap"), (dict(Q=wide.transpose(0, 1)[:4].transpose(0, 1)[:, :, ::1].cpu()), "CUDA"),
+                     (dict(Q=torch.zeros((p.n_tokens, 4, 128), dtype=torch.bfloat16, device="cuda")[:, :, ::2]), "contiguous"),
+                     (dict(k_cache=b.k_cache[:-1]), "elements"), (dict(v_cache=b.v_cache.transpose(0, 1)), "contiguous"),
+                     (dict(block_table=b.table.long()), "int32"), (dict(cu_new=b.cu[:-1]), "elements"), (dict(O=b.O[:, :2]), "contiguous"),
+                     (dict(lse=torch.zeros(3, device="cuda")), "elements"), (dict(workspace=b.ws.float()), "uint8"),
+                     (dict(kv_len=b.kv_len.cpu()), "CUDA")):
+        with pytest.raises(ValueError, match=why):
+            attn(**bad)
+    with pytest.raises(C.CobsError, match="workspace"):
+        attn(workspace=b.ws[:1024])
+    with pytest.raises(AttributeError):
+        C.cobs_paged_append(p, wide[:, :2], wide[:, 2:4], torch.full((p.n_tokens,), -1, dtype=torch.int32, device="cuda"), b.k_cache,
+                            b.v_cache, stream=5)
+    with pytest.raises(ValueError, match="stride"):
+        C.cobs_paged_append(p, wide[:, :2], wide[:, 2:4].contiguous(), torch.full((p.n_tokens,), -1, dtype=torch.int32, device="cuda"),
+                            b.k_cache, b.v_cache)
+
+
 def test_steps_of_a_serving_loop():
     """Three requests live through prompt chunks and single tokens; each step's tables, append and
     attention run as one paged_step, checked against a contiguous history."""

@@ -108,19 +108,20 @@ def test_binding_refuses_host_tensors(lib):
         lib.cobs_paged_tables(p, z, z, z, z, z, z, z, z, z)
     with pytest.raises(ValueError, match="CUDA"):
         lib.cobs_paged_attn(p, z, z, z, z, z, z, z, None, z)
+    with pytest.raises(TypeError, match="tensor"):
+        lib.cobs_paged_append(p, z, z, z, None, z)
 
 
-def test_token_rows_must_keep_a_tokens_heads_together(lib):
+def test_params_of_the_binding(lib):
+    import dataclasses
     p = _p(lib)
-    wide = torch.zeros((16, 12, 128), dtype=torch.bfloat16)
-    rows = lib._rows(wide[:, :8], "Q", p, 8, -1)
-    assert rows == (wide.data_ptr(), 12 * 128)
-    assert lib._rows(wide[:, :8].contiguous(), "Q", p, 8, -1)[1] == 0
-    for bad in (wide[:, ::2][:, :6], wide.transpose(0, 1)[:8].transpose(0, 1)[:15], wide[:, :8].float(),
-                torch.zeros((16, 8, 256), dtype=torch.bfloat16)[:, :, ::2], torch.zeros((1, 8, 128), dtype=torch.bfloat16).expand(16, 8, 128),
-                torch.zeros((8, 16, 128), dtype=torch.bfloat16).transpose(0, 1)):
-        with pytest.raises(ValueError):
-            lib._rows(bad, "Q", p, 8, -1)
+    c = p.c(5000, 3000)
+    assert (c.R, c.n_tokens, c.dtype, c.q_stride, c.kv_stride) == (4, 16, lib.COBS_BF16, 5000, 3000)
+    assert p.c().q_stride == 0   # the copy above has not changed the params
+    q = dataclasses.replace(p, max_new=7)
+    assert q.c().max_new == 7 and q.address != p.address and p.c().max_new == 4
+    with pytest.raises(dataclasses.FrozenInstanceError):
+        p.R = 5
 
 
 def test_tables_walk_by_hand(lib):
