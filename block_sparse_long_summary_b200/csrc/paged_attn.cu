@@ -10,6 +10,16 @@ namespace {
 
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
+// float32 stays on the CUDA cores. bf16 with one token per request has at most 16 rows against each key
+// and is a matter of reading the cache: warps with mma.sync take 8 x 32k keys in 168 us where the
+// 128-row tcgen05 tiles take 195 us, one request at 4k keys 10.4 against 15.9 us, 62 ragged ones 67
+// against 95 us. Everything else takes the 128-row tiles.
+enum Kernel { kSimt, kChunk, kDecode };
+Kernel kernel_of(const PagedDims& m) {
+    if (m.dtype != COBS_BF16) return kSimt;
+    return m.max_new == 1 ? kDecode : kChunk;
+}
+
 struct Layout {
     int workers, rec_rows;
     size_t seg_bytes, rec_bytes;
@@ -17,9 +27,11 @@ struct Layout {
 
 Layout layout_of(const PagedDims& m) {
     Layout l;
-    const bool tensor = m.dtype == COBS_BF16;
-    l.workers = tensor ? paged_chunk_workers(m) : paged_simt_workers(m);
-    l.rec_rows = tensor ? paged_chunk_rec_rows(m) : paged_simt_rec_rows(m);
+    switch (kernel_of(m)) {
+        case kSimt: l.workers = paged_simt_workers(m); l.rec_rows = paged_simt_rec_rows(m); break;
+        case kDecode: l.workers = paged_decode_workers(m); l.rec_rows = paged_decode_rec_rows(m); break;
+        default: l.workers = paged_chunk_workers(m); l.rec_rows = paged_chunk_rec_rows(m);
+    }
     l.seg_bytes = al256((size_t)l.workers * sizeof(PagedSeg));
     l.rec_bytes = (size_t)l.workers * 2 * l.rec_rows * (m.d + 2) * sizeof(float);
     return l;
@@ -47,7 +59,11 @@ cudaError_t launch_paged_attn(const PagedDims& m, const void* Q, const void* k_c
     a.n_pages = m.n_pages; a.max_pages = m.max_pages; a.n_tokens = m.n_tokens; a.max_new = m.max_new;
     a.W = m.W; a.S = m.S;
     a.sl2 = (float)(1.4426950408889634 / sqrt((double)m.d));
-    if (m.dtype == COBS_BF16) return launch_paged_chunk(m, a, Q, k_cache, v_cache, s);
+    switch (kernel_of(m)) {
+        case kChunk: a.lead_one = 3; a.lead_two = 6; return launch_paged_chunk(m, a, Q, k_cache, v_cache, s);
+        case kDecode: a.lead_one = a.lead_two = 2; return launch_paged_decode(m, a, Q, k_cache, v_cache, s);
+        default: a.lead_one = a.lead_two = 3;
+    }
     return launch_paged_simt(m, a, static_cast<const float*>(Q), static_cast<const float*>(k_cache), static_cast<const float*>(v_cache), s);
 }
 

@@ -20,4 +20,10 @@ int paged_chunk_workers(const PagedDims& m);
 cudaError_t launch_paged_chunk(const PagedDims& m, const PagedArgs& a, const void* Q, const void* kc, const void* vc,
                                cudaStream_t s);
 
+// bf16, one new token per request.
+int paged_decode_rec_rows(const PagedDims& m);
+int paged_decode_workers(const PagedDims& m);
+cudaError_t launch_paged_decode(const PagedDims& m, const PagedArgs& a, const void* Q, const void* kc, const void* vc,
+                                cudaStream_t s);
+
 }  // namespace cobs

@@ -43,6 +43,7 @@ struct PagedArgs {
     int rec_rows;
     int* err;
     int R, Hq, Hkv, G, page, page_shift, n_pages, max_pages, n_tokens, max_new, W, S;
+    int lead_one, lead_two; // a unit's start and end in tiles, for one and two row tiles (measured at 1, 2, 3 and 6)
     float sl2;              // log2(e) / sqrt(d)
 };
 
@@ -72,7 +73,7 @@ struct PagedEntry {
 
 template <int KT>
 __device__ __forceinline__ void entry_tiles(const PagedArgs& a, int TQ, PagedEntry& e) {
-    e.lead = 2 * e.n > TQ ? 6 : 3;  // (measured at 1, 3 and 6 for both)
+    e.lead = 2 * e.n > TQ ? a.lead_two : a.lead_one;
 
     const int hi = e.last_pos();
     e.lo = a.W > 0 ? max(0, e.pos0 - a.W + 1) : 0;
