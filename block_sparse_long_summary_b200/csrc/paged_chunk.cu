@@ -48,7 +48,7 @@ template <int STAGES>
 struct Misc {
     uint64_t barQ, barQfree, barKV[STAGES], barFree[STAGES], barS[2], barP[2], barO[2], barFix[kFixDepth], barDone;
     long long tmp[2 * kThreads / 32];
-    PagedRange range;
+    PagedStart<kKT> start;
     int dirty[kFixDepth][2];
     uint32_t tmem;
     float row[2][2][128];  // [group][half of the columns][row]: maxima of a tile, sums and maxima of a unit
@@ -235,17 +235,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         mbar_init(&barDone, 1);
         fence_barrier_init();
     }
-    plan_range<kThreads, kKT>(a, TQ, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sKV), sh_.tmp, &sh_.range);
+    allow_merge();
+    plan_start<kThreads, kKT>(a, TQ, blockIdx.x, gridDim.x, kLoadWarp, reinterpret_cast<int*>(sKV), sh_.tmp, &sh_.start);
     fence_proxy_async();  // the plan's use of the ring before TMA's
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const PagedRange rg = sh_.range;
     const uint32_t tmem = sh_.tmem;
     bool ok = true;
-    PagedWalk<kKT> w;
-    bool more = w.first(a, TQ, rg);
-    if (tid == kFixWarp * 32 + 32) a.seg[blockIdx.x] = w.seg(a, rg, blockIdx.x);
+    PagedWalk<kKT> w = sh_.start.walk;
+    bool more = sh_.start.more;
+    if (tid == kFixWarp * 32 + 32) a.seg[blockIdx.x] = w.seg(a, sh_.start.range, blockIdx.x);
 
     if (warp < 16) {
         // ------------------------------------------------------------ softmax and epilogue of row tile g
@@ -278,10 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 if (ok) ok = wait_on(&barS[g], nS & 1, a.err);
                 ++nS;
                 int dirty = 0;  // the stage of V (from 1) where this thread forms the product
-                if (masked && ok) {  // (after S: the tiles before this one have then been prepared)
-                    ok = wait_on(&barFix[fix % kFixDepth], (fix / kFixDepth) & 1, a.err);
-                    dirty = max(dirty_sh[fix % kFixDepth][0], dirty_sh[fix % kFixDepth][1]);
-                }
                 tc::fence_after_sync();
                 if (warp_live) {
                     const int hi = t - j0, lo = a.W > 0 ? hi - a.W + 1 : 0, sk = a.W > 0 ? a.S - j0 : 0;
@@ -330,6 +326,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     }
                     if (grow) m = mt;
                     const float neg = m == -INFINITY ? 0.0f : -m;
+                    if (masked && ok) {  // (after S: the tiles before this one have then been prepared)
+                        ok = wait_on(&barFix[fix % kFixDepth], (fix / kFixDepth) & 1, a.err);
+                        dirty = max(dirty_sh[fix % kFixDepth][0], dirty_sh[fix % kFixDepth][1]);
+                    }
                     // p = 2^(s c - m) of 32 keys at a time; P, half as wide, over this half's own scores
                     float2 ps[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     const float2 scale = make_float2(sl2, sl2), shift = make_float2(neg, neg);
@@ -689,16 +689,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                         zero(n_hi, kKT);
                         fence_proxy_async();
                         uint32_t inf = 0;  // an exponent of all ones carries into its sign bit
-                        auto look = [&](int from, int to) {
-                            for (int c = 8 * from + f; c < 8 * to; c += 256)
+                        auto look = [&](int from, int to) {  // (two chunks of each half a turn: little code, run seldom)
+#pragma unroll 1
+                            for (int c = 8 * from + f; c < 8 * to; c += 128)
 #pragma unroll
-                                for (int y = 0; y < 4; ++y)
-#pragma unroll
-                                    for (int h = 0; h < C::H; ++h) {
-                                        const uint4 v = *reinterpret_cast<const uint4*>(sV + h * kBox + (size_t)min(c + 64 * y, 8 * to - 1) * 16);
-                                        inf |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
-                                               ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
-                                    }
+                                for (int y = 0; y < 2 * C::H; ++y) {
+                                    const int at = min(c + 64 * (y & 1), 8 * to - 1);
+                                    const uint4 v = *reinterpret_cast<const uint4*>(sV + (y >> 1) * kBox + (size_t)at * 16);
+                                    inf |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                                           ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+                                }
                         };
                         if (e.n > 1) {  // (a single token's rows see the same keys)
                             look(0, n_sink);
@@ -732,6 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 template <int D>
 cudaError_t run(const PagedDims& m, const PagedArgs& a, const void* Q, const void* kc, const void* vc, cudaStream_t s) {
     using C = Cfg<D>;
+    static_assert(C::kSmem <= 227 * 1024, "shared memory");
+    static_assert((kMaxRequests + 1) * 4 <= C::kStages * C::kTile, "the plan's scratch");
     const int TM = 128 / m.G, workers = sm_count();
     ChunkMaps maps;
     const uint64_t qd[3] = {(uint64_t)D, (uint64_t)m.Hq, (uint64_t)m.n_tokens}, qs[2] = {(uint64_t)D * 2, (uint64_t)m.q_stride * 2};

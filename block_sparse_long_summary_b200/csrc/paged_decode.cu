@@ -49,18 +49,17 @@ __global__ void __launch_bounds__(kT, 1) paged_decode_kernel(PagedArgs a, const 
     using C = Cfg<D, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long tmp[2 * kT / 32];
-    __shared__ PagedRange range_sh;
+    __shared__ PagedStart<kKT> start;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    plan_range<kT, kKT>(a, 1, blockIdx.x, gridDim.x, reinterpret_cast<int*>(smem), tmp, &range_sh);
-    const PagedRange range = range_sh;
+    allow_merge();
+    plan_start<kT, kKT>(a, 1, blockIdx.x, gridDim.x, 0, reinterpret_cast<int*>(smem), tmp, &start);
     unsigned char* ring = smem + warp * C::kStages * C::kStage;
     float* join = reinterpret_cast<float*>(smem + C::kRing);  // [warp][head][kRow]
     float2* ml = reinterpret_cast<float2*>(join + kWarps * 8 * NT * C::kRow);  // [warp][head]
 
-    PagedWalk<kKT> w, f;  // the unit in hand, and the one whose tiles are being fetched
-    bool more = w.first(a, 1, range);
-    if (tid == 0) a.seg[blockIdx.x] = w.seg(a, range, blockIdx.x);
-    f = w;
+    PagedWalk<kKT> w = start.walk, f = w;  // the unit in hand, and the one whose tiles are being fetched
+    bool more = start.more;
+    if (tid == 0) a.seg[blockIdx.x] = w.seg(a, start.range, blockIdx.x);
     bool fetching = more;
     int ft = f.t0;          // tile to look up next
     int page = -1, j = 0;   // page and first key of the slice looked up last (-1: nothing to copy)

@@ -149,109 +149,6 @@ __device__ __forceinline__ long long block_scan(long long v, long long* tmp, lon
     return v + before;
 }
 
-// Worker w's range where every one of at most 32 requests is one entry: lane r of each warp looks after
-// request r, so no warp waits for another (a small call spends most of its time on such steps).
-// Returns whether the case is that one.
-template <int KT>
-__device__ __forceinline__ bool plan_small(const PagedArgs& a, int TQ, int w, int n_workers, PagedRange& out) {
-    if (a.R > 32) return false;
-    const int lane = threadIdx.x & 31;
-    int row0 = 0, n = 0, L = 0;
-    bool bad = false;
-    if (lane < a.R) request_of(a, lane, row0, n, L, bad);
-    if (__any_sync(kFull, n > TQ)) return false;
-    if (bad && w == 0) report_error(a.err, kErrBadLength);
-    const long long cost = n > 0 ? (long long)make_entry<KT>(a, lane, 0, TQ, row0, n, L).cost() * a.Hkv : 0;
-    long long inc = cost;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += u;
-    }
-    const long long total = __shfl_sync(kFull, inc, 31);
-    const int n_eff = (int)min((long long)n_workers, total);
-    out = PagedRange{0, 0, 0, 0, 0, total, n_eff};
-    if (w < n_eff) {
-        const long long b0 = share_of(total, w, n_eff), b1 = share_of(total, w + 1, n_eff);
-        out.b0 = b0;
-        out.r = __ffs(__ballot_sync(kFull, b0 >= inc - cost && b0 < inc)) - 1;
-        out.off = (int)(b0 - __shfl_sync(kFull, inc - cost, out.r));
-        out.count = (int)(b1 - b0);
-    }
-    return true;
-}
-
-// Worker w's range, by all T threads of the block. scratch: R + 1 ints; tmp: 2 T / 32 values.
-template <int T, int KT>
-__device__ __forceinline__ void plan_range(const PagedArgs& a, int TQ, int w, int n_workers, int* scratch,
-                                           long long* tmp, PagedRange* out) {
-    PagedRange small;
-    if (plan_small<KT>(a, TQ, w, n_workers, small)) {
-        if (threadIdx.x == 0) *out = small;
-        __syncthreads();
-        return;
-    }
-    const int tid = threadIdx.x;
-    int turn = 0;  // the scans' halves of tmp
-    auto scan = [&](long long v, long long& tot) { return block_scan<T>(v, tmp + (turn ^= 1) * (T / 32), tot); };
-    // entries before each request
-    long long base = 0;
-    for (int r0 = 0; r0 < a.R; r0 += T) {
-        const int r = r0 + tid;
-        int row0, n = 0, L;
-        bool bad = false;
-        if (r < a.R) request_of(a, r, row0, n, L, bad);
-        if (bad && w == 0) report_error(a.err, kErrBadLength);
-        long long tot;
-        const long long inc = scan((n + TQ - 1) / TQ, tot);
-        if (r < a.R) scratch[r + 1] = (int)(base + inc);
-        base += tot;
-    }
-    if (tid == 0) {
-        scratch[0] = 0;
-        *out = PagedRange{0, 0, 0, 0, 0, 0, 0};
-    }
-    __syncthreads();
-    const int E = (int)base;
-    auto cost_of = [&](int e, int& r, int& i) -> int {
-        int lo = 0, hi = a.R - 1;  // the last request whose first entry is <= e
-        while (lo < hi) {          // (requests without entries share their successor's number)
-            const int mid = (lo + hi + 1) >> 1;
-            if (scratch[mid] <= e) lo = mid; else hi = mid - 1;
-        }
-        int row0, n, L;
-        bool bad;
-        request_of(a, lo, row0, n, L, bad);
-        r = lo;
-        i = e - scratch[lo];
-        return make_entry<KT>(a, r, i, TQ, row0, n, L).cost() * a.Hkv;
-    };
-    long long total = 0;
-    int r = 0, i = 0, cost = 0;
-    long long inc = 0;
-    for (int e0 = 0; e0 < E; e0 += T) {
-        cost = e0 + tid < E ? cost_of(e0 + tid, r, i) : 0;
-        long long tot;
-        inc = scan(cost, tot);
-        total += tot;
-    }
-    const int n_eff = (int)min((long long)n_workers, total);
-    if (w >= n_eff) return;  // (the whole block)
-    const long long b0 = share_of(total, w, n_eff), b1 = share_of(total, w + 1, n_eff);
-    long long before = 0;
-    for (int e0 = 0; e0 < E; e0 += T) {
-        if (E > T) {  // else the values of the only round above still stand
-            cost = e0 + tid < E ? cost_of(e0 + tid, r, i) : 0;
-            long long tot;
-            inc = scan(cost, tot) + before;
-            before += tot;
-        }
-        if (b0 >= inc - cost && b0 < inc)
-            *out = PagedRange{r, i, (int)(b0 - (inc - cost)), (int)(b1 - b0), b0, total, n_eff};
-    }
-    __syncthreads();
-}
-
 // A worker's walk over the units of its range that have tiles in it.
 template <int KT>
 struct PagedWalk {
@@ -309,6 +206,164 @@ struct PagedWalk {
     }
 };
 
+// What a worker starts from: its range, and its walk at the first unit.
+template <int KT>
+struct PagedStart {
+    PagedRange range;
+    PagedWalk<KT> walk;
+    int more;      // whether there is a unit
+    int ready;     // of the warp's attempt below
+    __device__ __forceinline__ void set(const PagedArgs& a, int TQ, const PagedRange& g) {  // by one thread
+        range = g;
+        more = walk.first(a, TQ, g);
+    }
+};
+
+// Worker w's start where there are at most 32 requests with at most kWarpEntries entries, by one warp: lane
+// r looks after request r, then lane i after entries i, i + 32, ... A small call waits for these steps, and
+// the warps beside it only add to what its scheduler has to issue. Returns whether the case is that one.
+constexpr int kWarpEntries = 256;
+
+template <int KT>
+__device__ __forceinline__ bool plan_warp(const PagedArgs& a, int TQ, int w, int n_workers, PagedStart<KT>* out) {
+    const int lane = threadIdx.x & 31;
+    int row0 = 0, n = 0, L = 0;
+    bool bad = false;
+    if (lane < a.R) request_of(a, lane, row0, n, L, bad);
+    if (bad && w == 0) report_error(a.err, kErrBadLength);
+    const int mine = (n + TQ - 1) / TQ;
+    int ends = mine;  // entries up to and with this request's
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, ends, o);
+        if (lane >= o) ends += u;
+    }
+    const int E = __shfl_sync(kFull, ends, 31);
+    if (E > kWarpEntries) return false;
+    const int begins = ends - mine;
+    int r = 0, i = 0;
+    long long cost = 0, inc = 0;
+    auto costs = [&](int e0) {  // this lane's entry of the 32 from e0 on, and the sum up to it
+        const int e = e0 + lane;
+        int lo = 0;  // requests that end at or before e
+#pragma unroll
+        for (int step = 16; step > 0; step >>= 1) {
+            const int x = __shfl_sync(kFull, ends, lo + step - 1);
+            if (x <= e) lo += step;
+        }
+        r = min(lo, 31);
+        i = e - __shfl_sync(kFull, begins, r);
+        const int rr = __shfl_sync(kFull, row0, r), rn = __shfl_sync(kFull, n, r), rL = __shfl_sync(kFull, L, r);
+        cost = e < E ? (long long)make_entry<KT>(a, r, i, TQ, rr, rn, rL).cost() * a.Hkv : 0;
+        inc = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += u;
+        }
+        return __shfl_sync(kFull, inc, 31);
+    };
+    long long total = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += 32) total += costs(e0);
+    const int n_eff = (int)min((long long)n_workers, total);
+    if (w >= n_eff) {
+        if (lane == 0) out->set(a, TQ, PagedRange{0, 0, 0, 0, 0, 0, 0});
+        return true;
+    }
+    const long long b0 = share_of(total, w, n_eff), b1 = share_of(total, w + 1, n_eff);
+    long long before = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const long long sum = E > 32 ? costs(e0) : total;  // (the values of the only round above still stand)
+        const long long at = b0 - before;
+        if (at >= inc - cost && at < inc)
+            out->set(a, TQ, PagedRange{r, i, (int)(at - (inc - cost)), (int)(b1 - b0), b0, total, n_eff});
+        before += sum;
+        if (before > b0) break;
+    }
+    return true;
+}
+
+// Worker w's start, for all T threads of the block; `planner` is the warp that tries alone. scratch: R + 1
+// ints; tmp: 2 T / 32 values; out: shared memory, to be read after the call.
+template <int T, int KT>
+__device__ __forceinline__ void plan_start(const PagedArgs& a, int TQ, int w, int n_workers, int planner, int* scratch,
+                                           long long* tmp, PagedStart<KT>* out) {
+    const int tid = threadIdx.x;
+    if (a.R <= 32) {
+        if (tid >> 5 == planner) {
+            const bool ok = plan_warp<KT>(a, TQ, w, n_workers, out);
+            if ((tid & 31) == 0) out->ready = ok;
+        }
+        __syncthreads();
+        if (out->ready) return;
+    }
+    int turn = 0;  // the scans' halves of tmp
+    auto scan = [&](long long v, long long& tot) { return block_scan<T>(v, tmp + (turn ^= 1) * (T / 32), tot); };
+    // entries before each request
+    long long base = 0;
+    for (int r0 = 0; r0 < a.R; r0 += T) {
+        const int r = r0 + tid;
+        int row0, n = 0, L;
+        bool bad = false;
+        if (r < a.R) request_of(a, r, row0, n, L, bad);
+        if (bad && w == 0) report_error(a.err, kErrBadLength);
+        long long tot;
+        const long long inc = scan((n + TQ - 1) / TQ, tot);
+        if (r < a.R) scratch[r + 1] = (int)(base + inc);
+        base += tot;
+    }
+    if (tid == 0) scratch[0] = 0;
+    __syncthreads();
+    const int E = (int)base;
+    auto cost_of = [&](int e, int& r, int& i) -> long long {
+        int lo = 0, hi = a.R - 1;  // the last request whose first entry is <= e
+        while (lo < hi) {          // (requests without entries share their successor's number)
+            const int mid = (lo + hi + 1) >> 1;
+            if (scratch[mid] <= e) lo = mid; else hi = mid - 1;
+        }
+        int row0, n, L;
+        bool bad;
+        request_of(a, lo, row0, n, L, bad);
+        r = lo;
+        i = e - scratch[lo];
+        return (long long)make_entry<KT>(a, r, i, TQ, row0, n, L).cost() * a.Hkv;
+    };
+    long long total = 0, cost = 0, inc = 0;
+    int r = 0, i = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += T) {
+        cost = e0 + tid < E ? cost_of(e0 + tid, r, i) : 0;
+        long long tot;
+        inc = scan(cost, tot);
+        total += tot;
+    }
+    const int n_eff = (int)min((long long)n_workers, total);
+    if (w >= n_eff) {
+        if (tid == 0) out->set(a, TQ, PagedRange{0, 0, 0, 0, 0, 0, 0});
+        __syncthreads();
+        return;
+    }
+    const long long b0 = share_of(total, w, n_eff), b1 = share_of(total, w + 1, n_eff);
+    long long before = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += T) {
+        if (E > T) {  // else the values of the only round above still stand
+            cost = e0 + tid < E ? cost_of(e0 + tid, r, i) : 0;
+            long long tot;
+            inc = scan(cost, tot) + before;
+            before += tot;
+        }
+        if (b0 >= inc - cost && b0 < inc)
+            out->set(a, TQ, PagedRange{r, i, (int)(b0 - (inc - cost)), (int)(b1 - b0), b0, total, n_eff});
+    }
+    __syncthreads();
+}
+
+// The merge may be launched (it waits for this grid's end by itself).
+__device__ __forceinline__ void allow_merge() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Page that holds key tokens [j, j + page): -1 behind the table, or (reported) outside the cache.
 __device__ __forceinline__ int page_of(const PagedArgs& a, int r, int slot, bool needed) {
     if (slot >= a.max_pages) return -1;
@@ -329,6 +384,7 @@ __device__ __forceinline__ int page_of(const PagedArgs& a, int r, int slot, bool
 template <typename T, int D>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedSeg* seg, const float* recs, T* O, float* lse, int rec_rows,
                                                           int Hq, int G) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float2 ml[2][16][8];
     const int tid = threadIdx.x, col = tid & 7, q = tid >> 3;
     const PagedSeg s = seg[blockIdx.x + 1];
@@ -413,10 +469,11 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedSeg* seg, c
     if (lse && q == 0) lse[orow] = empty ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
-// The merge after an attention grid of `workers` ranges whose units have at most `rows` rows. (As a
-// programmatic dependent of that grid it measured 4 us slower per call: 24.0 against 19.5 us for one
-// token at 4k keys.) It asks for the attention grid's division of the SM's memory, so that an SM need
-// not change it between the two.
+// The merge after an attention grid of `workers` ranges whose units have at most `rows` rows, as its
+// programmatic dependent: that grid allows it from its own start, so that the launch is over with when
+// the records are complete (one token at 4k keys 14.3 -> 12.3 us per call; allowed at the grid's end it
+// was slower than a plain launch). It asks for the attention grid's division of the SM's memory, so that
+// an SM need not change it between the two.
 template <typename T, int D>
 cudaError_t launch_paged_merge(const PagedArgs& a, int workers, int rows, cudaStream_t s) {
     if (workers < 2) return cudaSuccess;
@@ -426,9 +483,17 @@ cudaError_t launch_paged_merge(const PagedArgs& a, int workers, int rows, cudaSt
     });
     if (e != cudaSuccess) return e;
     count_launch();
-    paged_merge_kernel<T, D><<<dim3(workers - 1, (rows + 7) / 8), 128, 0, s>>>(a.seg, a.rec, static_cast<T*>(a.O), a.lse, a.rec_rows,
-                                                                               a.Hq, a.G);
-    return cudaGetLastError();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(workers - 1, (rows + 7) / 8);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, (const PagedSeg*)a.seg, (const float*)a.rec, static_cast<T*>(a.O), a.lse,
+                              a.rec_rows, a.Hq, a.G);
 }
 
 }  // namespace cobs

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kT, blocks_per_sm(D, M)) paged_simt_kernel(Pag
                                                         const float* kc, const float* vc) {
     extern __shared__ __align__(16) float sm[];
     __shared__ long long tmp[2 * kT / 32];
-    __shared__ PagedRange range;
+    __shared__ PagedStart<kKT> start;
     __shared__ int page_sh[2][kKT / 16];
     constexpr int RM = M / 16, CD = D / 16, KS = D + 4;
     float* sQ = sm;               // [M][D + 4]
@@ -54,12 +54,12 @@ __global__ void __launch_bounds__(kT, blocks_per_sm(D, M)) paged_simt_kernel(Pag
     float* sP = sV + kKT * D;     // [M][68]
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int TQ = M / a.G;
-    plan_range<kT, kKT>(a, TQ, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm), tmp, &range);
-    const PagedRange g = range;
-    PagedWalk<kKT> w;
+    allow_merge();
+    plan_start<kT, kKT>(a, TQ, blockIdx.x, gridDim.x, 0, reinterpret_cast<int*>(sm), tmp, &start);
+    PagedWalk<kKT> w = start.walk;
     int piece = 0;
-    bool more = w.first(a, TQ, g);
-    if (tid == 0) a.seg[blockIdx.x] = w.seg(a, g, blockIdx.x);
+    bool more = start.more;
+    if (tid == 0) a.seg[blockIdx.x] = w.seg(a, start.range, blockIdx.x);
     for (; more; more = w.next(a, TQ), ++piece) {
         const PagedEntry& e = w.e;
         const int rows = e.n * a.G, hi = e.last_pos();
