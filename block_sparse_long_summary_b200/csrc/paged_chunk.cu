@@ -190,9 +190,10 @@ struct ChunkMaps {
 };
 
 // A tile some row of the unit does not see in full.
-__device__ __forceinline__ bool masked_tile(const PagedArgs& a, const PagedEntry& e, int j0) {
-    return !(j0 + kKT - 1 <= e.pos0 && (a.W <= 0 || e.last_pos() - j0 < a.W));
+__device__ __forceinline__ bool masked_tile(const PagedArgs& a, int pos0, int n, int j0) {
+    return !(j0 + kKT - 1 <= pos0 && (a.W <= 0 || pos0 + n - 1 - j0 < a.W));
 }
+__device__ __forceinline__ bool masked_tile(const PagedArgs& a, const PagedEntry& e, int j0) { return masked_tile(a, e.pos0, e.n, j0); }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ ChunkMaps maps, PagedArgs a) {
@@ -258,23 +259,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         uint32_t nS = 0, nO = 0, nFix = 0;
         Pos<C::kStages> at;  // of the unit's first tile
         int piece = 0;
-        for (; more; more = w.next(a, TQ), ++piece) {
-            const PagedEntry& e = w.e;
-            const Shape<kKT> sh(a, w, TM);
+        // The walk lies in local memory behind a pointer the compiler cannot see through: of its 17 registers
+        // the loop over the tiles needs six, and left to itself the compiler spilled in that loop.
+        PagedWalk<kKT>* pw = &w;
+        asm volatile("" : "+l"(pw)::"memory");
+        for (; more; more = pw->next(a, TQ), ++piece) {
+            const int pos0 = pw->e.pos0, en = pw->e.n, t0 = pw->t0, t1 = pw->t1, sT = pw->e.sT, loT = pw->e.loT;
+            const Shape<kKT> sh(a, *pw, TM);
             const bool pair = sh.pair;
             const int tok0 = pair ? 0 : g * TM;       // first token of this group's rows
-            const int ntok = min(TM, e.n - tok0);
+            const int ntok = min(TM, en - tok0);
             const bool live = tok < ntok;
             const bool warp_live = (warp & 3) * 32 < ntok * a.G;
-            const int t = e.pos0 + tok0 + tok;
+            const int t = pos0 + tok0 + tok;
             float m = -INFINITY, l = 0.0f;
-            const int kg = w.t0 + (pair ? g : 0);  // this group's first tile
-            for (int k = w.t0; k < w.t1; ++k) {
-                const int j0 = e.key_tile(k) * kKT;
-                const bool masked = masked_tile(a, e, j0);
+            const int kg = t0 + (pair ? g : 0);  // this group's first tile
+            for (int k = t0; k < t1; ++k) {
+                const int j0 = (k < sT ? k : loT + (k - sT)) * kKT;
+                const bool masked = masked_tile(a, pos0, en, j0);
                 const uint32_t fix = nFix;
                 nFix += masked;
-                if (pair && ((k - w.t0) & 1) != g) continue;
+                if (pair && ((k - t0) & 1) != g) continue;
                 if (ok) ok = wait_on(&barS[g], nS & 1, a.err);
                 ++nS;
                 int dirty = 0;  // the stage of V (from 1) where this thread forms the product
@@ -394,12 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&barP[g]);
             }
-            const bool any = kg < w.t1;  // (a pair's second group may have no tile)
+            const bool any = kg < t1;  // (a pair's second group may have no tile)
             if (any) {
                 if (ok) ok = wait_on(&barO[g], nO & 1, a.err);
                 ++nO;
             }
-            at.advance(2 * (w.t1 - w.t0));  // the output's first stage
+            at.advance(2 * (t1 - t0));  // the output's first stage
             const Pos<C::kStages> mine = at.plus(pair ? 0 : g);
             at.advance(sh.stages);
             if (ok && sh.staged) ok = wait_on(&barKV[mine.s], mine.ph, a.err);
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             // The threads of one row are in warps of the same TMEM lanes: two of each group, each with a share
             // of the columns, of both accumulators if the unit's tiles went to both groups.
             float f0 = 1.0f, f1 = 0.0f;  // factors of O_0 and O_1 (of O_g alone, if not both)
-            const bool both = pair && w.t1 - w.t0 > 1, empty = t < 0, whole = w.whole();
+            const bool both = pair && t1 - t0 > 1, empty = t < 0, whole = pw->whole();
             if (warp_live && any) {
                 auto meet = [&] { if (both) rows_sync<128>(9 + (warp & 3)); else rows_sync<64>(1 + 4 * g + (warp & 3)); };
                 row_sh[g][half][row] = l;
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 }
                 meet();  // before the slots are written again
                 const int c0 = both ? 32 * (2 * g + half) : half * (D / 2), c1 = both ? min(c0 + 32, D) : c0 + D / 2;
-                const size_t orow = (size_t)(e.row0 + tok0 + (live ? tok : 0)) * a.Hq + w.h * a.G + (live ? hrow : 0);
+                const size_t orow = (size_t)(pw->e.row0 + tok0 + (live ? tok : 0)) * a.Hq + pw->h * a.G + (live ? hrow : 0);
                 float* rec = a.rec + ((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * a.rec_rows * (D + 2);
                 const int rrow = live ? (tok0 + tok) * a.G + hrow : 0;
                 unsigned char* out = sh.staged ? sKV + (size_t)mine.s * C::kTile + row * (2 * D)
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 if ((warp & 3) == 0 && half == 0 && (!pair || g == 0)) {  // a token's rows of the group are one run of both memories
                     const unsigned char* src = sKV + (size_t)mine.s * C::kTile;
                     for (int i = lane; i < ntok; i += 32)
-                        bulk_s2g(static_cast<__nv_bfloat16*>(a.O) + ((size_t)(e.row0 + tok0 + i) * a.Hq + w.h * a.G) * D,
+                        bulk_s2g(static_cast<__nv_bfloat16*>(a.O) + ((size_t)(pw->e.row0 + tok0 + i) * a.Hq + pw->h * a.G) * D,
                                  src + (size_t)i * a.G * 2 * D, a.G * 2 * D);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
