@@ -6,8 +6,9 @@
 // A block of 256 threads walks its range of (unit, 64-key tile) pairs. The unit's rows (tokens x
 // the G heads of the group) are M = 64 or 16 rows; thread (ty, tx) of 16 x 16 holds M / 16 rows x
 // 4 keys of the scores and M / 16 rows x d / 16 columns of the output in registers, and each row's
-// running maximum and sum. K of the next tile is in flight (cp.async) while the softmax and P V of
-// this one run, V of this tile while its scores are formed. The float32 products stay on the FMA
+// running maximum and sum. V of a tile is in flight (cp.async) while its scores are formed; P takes K's
+// place, so that two blocks fit an SM at d = 128 and one computes while the other waits for K or at a
+// barrier. The float32 products stay on the FMA
 // pipes: the tensor cores' tf32 would drop 13 bits of each factor.
 #include <algorithm>
 #include <type_traits>
@@ -33,12 +34,12 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 
 template <int D, int M>
 constexpr size_t simt_smem() {
-    return sizeof(float) * ((size_t)M * (D + 4) + (size_t)kKT * (D + 4) + (size_t)kKT * D + (size_t)M * kPS);
+    return sizeof(float) * ((size_t)M * (D + 4) + (size_t)kKT * (D + 4) + (size_t)kKT * D);  // P (M x kPS) in K's place
 }
 
 // Blocks resident on an SM (shared memory and registers): one waits for its copies and its barriers, the
 // others compute.
-constexpr int blocks_per_sm(int d, int m) { return m == 16 ? (d == 64 ? 3 : 2) : (d == 64 ? 2 : 1); }
+constexpr int blocks_per_sm(int d, int m) { return m == 16 ? (d == 64 ? 3 : 2) : 2; }
 
 template <int D, int M>
 __global__ void __launch_bounds__(kT, blocks_per_sm(D, M)) paged_simt_kernel(PagedArgs a, const float* Q, long long q_stride,
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(kT, blocks_per_sm(D, M)) paged_simt_kernel(Pag
     float* sQ = sm;               // [M][D + 4]
     float* sK = sQ + M * KS;      // [64][D + 4]
     float* sV = sK + kKT * KS;    // [64][D]
-    float* sP = sV + kKT * D;     // [M][68]
+    float* sP = sK;               // [M][68]
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const int TQ = M / a.G;
     allow_merge();
@@ -127,8 +128,6 @@ __global__ void __launch_bounds__(kT, blocks_per_sm(D, M)) paged_simt_kernel(Pag
                 }
             }
             __syncthreads();  // K has been read
-            if (k + 1 < w.t1) load(sK, KS, kc, k + 1);
-            cp_commit();
             // a tile that every row sees in full needs no masks
             const bool full = j0 + kKT - 1 <= e.pos0 && (a.W <= 0 || hi - j0 < a.W);
 #pragma unroll
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(kT, blocks_per_sm(D, M)) paged_simt_kernel(Pag
 #pragma unroll
                 for (int x = 0; x < CD; ++x) o[y][x] *= f;
             }
-            cp_wait<1>();  // V
+            cp_wait<0>();  // V
             __syncthreads();
             // a hidden key adds nothing, whatever its value holds: tiles with masks test every pair (the test
             // costs as much as the products, so the others do without)
@@ -185,6 +184,8 @@ __global__ void __launch_bounds__(kT, blocks_per_sm(D, M)) paged_simt_kernel(Pag
             };
             if (full) product(std::false_type()); else product(std::true_type());
             __syncthreads();  // V and P have been read
+            if (k + 1 < w.t1) load(sK, KS, kc, k + 1);
+            cp_commit();
         }
         const bool whole = w.whole();
         const int slot = piece == 0 ? 0 : 1;
