@@ -24,7 +24,7 @@ BINDING = os.path.join(LIB_DIR, "_paged.so")
 BINDING_SRC = "paged_binding.cpp"
 SOURCES = ["api.cu", "summary.cu", "select.cu", "decode.cu", "decode_stream.cu", "decode_step.cu", "tma.cu", "prefill.cu",
            "mass.cu", "basis.cu", "paged_tables.cu", "paged_attn.cu", "paged_simt.cu",
-           "paged_chunk.cu", "paged_decode.cu"]
+           "paged_chunk.cu", "paged_decode.cu", "paged_decode_f32.cu"]
 HEADERS = ["common.cuh", "attn.cuh", "dims.h", "tma.h", "tc.cuh", "select_core.cuh", "stream_tile.cuh",
            "paged.h", "paged_kernels.h", "paged_plan.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -10,15 +10,12 @@ namespace {
 
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
-// float32 stays on the CUDA cores. bf16 with one token per request has at most 16 rows against each key
+// float32 stays on the CUDA cores. One token per request has at most 16 rows against each key
 // and is a matter of reading the cache: warps with mma.sync take 8 x 32k keys in 168 us where the
 // 128-row tcgen05 tiles take 195 us, one request at 4k keys 10.4 against 15.9 us, 62 ragged ones 67
 // against 95 us. Everything else takes the 128-row tiles.
 enum Kernel { kSimt, kChunk, kDecode };
-Kernel kernel_of(const PagedDims& m) {
-    if (m.dtype != COBS_BF16) return kSimt;
-    return m.max_new == 1 ? kDecode : kChunk;
-}
+Kernel kernel_of(const PagedDims& m) { return m.max_new == 1 ? kDecode : m.dtype == COBS_BF16 ? kChunk : kSimt; }
 
 struct Layout {
     int workers, rec_rows;
@@ -61,7 +58,11 @@ cudaError_t launch_paged_attn(const PagedDims& m, const void* Q, const void* k_c
     a.sl2 = (float)(1.4426950408889634 / sqrt((double)m.d));
     switch (kernel_of(m)) {
         case kChunk: a.lead_one = 3; a.lead_two = 6; return launch_paged_chunk(m, a, Q, k_cache, v_cache, s);
-        case kDecode: a.lead_one = a.lead_two = 2; return launch_paged_decode(m, a, Q, k_cache, v_cache, s);
+        case kDecode:
+            a.lead_one = a.lead_two = 2;
+            if (m.dtype == COBS_BF16) return launch_paged_decode(m, a, Q, k_cache, v_cache, s);
+            return launch_paged_decode_f32(m, a, static_cast<const float*>(Q), static_cast<const float*>(k_cache),
+                                           static_cast<const float*>(v_cache), s);
         default: a.lead_one = a.lead_two = 3;
     }
     return launch_paged_simt(m, a, static_cast<const float*>(Q), static_cast<const float*>(k_cache), static_cast<const float*>(v_cache), s);

@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(kT, 1) paged_decode_kernel(PagedArgs a, const 
                                 }
                             }
                 }
-                uint32_t pb[NT][2];
+                // p in two bf16 parts: its rounding is then 2^-17, next to nothing beside o's (with one part the
+                // error against 64 bits was 1.4 times that of o's rounding; the time is the same)
+                uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const float u0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], u1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
@@ -205,8 +207,11 @@ __global__ void __launch_bounds__(kT, 1) paged_decode_kernel(PagedArgs a, const 
                     const float p2 = exp2_fast(s[n][2] - u0), p3 = exp2_fast(s[n][3] - u1);
                     l[n][0] += p0 + p2;
                     l[n][1] += p1 + p3;
-                    pb[n][0] = movmatrix_trans(pack_bf16(p0, p1));
-                    pb[n][1] = movmatrix_trans(pack_bf16(p2, p3));
+                    const uint32_t a0 = pack_bf16(p0, p1), a1 = pack_bf16(p2, p3);
+                    pb[n][0] = movmatrix_trans(a0);
+                    pb[n][1] = movmatrix_trans(a1);
+                    pl[n][0] = movmatrix_trans(pack_bf16(p0 - __uint_as_float(a0 << 16), p1 - __uint_as_float(a0 & 0xffff0000u)));
+                    pl[n][1] = movmatrix_trans(pack_bf16(p2 - __uint_as_float(a1 << 16), p3 - __uint_as_float(a1 & 0xffff0000u)));
                 }
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t) {
@@ -214,7 +219,10 @@ __global__ void __launch_bounds__(kT, 1) paged_decode_kernel(PagedArgs a, const 
                     uint32_t av[4];
                     ldmatrix_x4_trans(av[0], av[1], av[2], av[3], sV + (t >> 2) * C::kHalf + r * 128 + ((cc ^ (r & 7)) << 4));
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_bf16_16816(o[n][t], av, pb[n][0], pb[n][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        mma_bf16_16816(o[n][t], av, pb[n][0], pb[n][1]);
+                        mma_bf16_16816(o[n][t], av, pl[n][0], pl[n][1]);
+                    }
                 }
             }
             __syncwarp();  // the stage has been read
