@@ -57,13 +57,13 @@ cudaError_t launch_paged_attn(const PagedDims& m, const void* Q, const void* k_c
     a.W = m.W; a.S = m.S;
     a.sl2 = (float)(1.4426950408889634 / sqrt((double)m.d));
     switch (kernel_of(m)) {
-        case kChunk: a.lead_one = 3; a.lead_two = 6; return launch_paged_chunk(m, a, Q, k_cache, v_cache, s);
+        case kChunk: a.lead_one = 2; a.lead_two = 3; return launch_paged_chunk(m, a, Q, k_cache, v_cache, s);
         case kDecode:
             a.lead_one = a.lead_two = 2;
             if (m.dtype == COBS_BF16) return launch_paged_decode(m, a, Q, k_cache, v_cache, s);
             return launch_paged_decode_f32(m, a, static_cast<const float*>(Q), static_cast<const float*>(k_cache),
                                            static_cast<const float*>(v_cache), s);
-        default: a.lead_one = a.lead_two = 3;
+        default: a.lead_one = a.lead_two = 1;
     }
     return launch_paged_simt(m, a, static_cast<const float*>(Q), static_cast<const float*>(k_cache), static_cast<const float*>(v_cache), s);
 }

@@ -43,7 +43,7 @@ struct PagedArgs {
     int rec_rows;
     int* err;
     int R, Hq, Hkv, G, page, page_shift, n_pages, max_pages, n_tokens, max_new, W, S;
-    int lead_one, lead_two; // a unit's start and end in tiles, for one and two row tiles (measured at 1, 2, 3 and 6)
+    int lead_one, lead_two; // a unit's start and end in tiles, for one and two row tiles (measured at 1 to 6)
     float sl2;              // log2(e) / sqrt(d)
 };
 
