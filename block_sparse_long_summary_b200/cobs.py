@@ -366,6 +366,9 @@ class PagedParams:
         object.__setattr__(self, "_struct", cp)
         object.__setattr__(self, "address", ctypes.addressof(cp))
 
+    def __reduce__(self):   # copies are made anew: the address is that of the object's own struct
+        return PagedParams, tuple(getattr(self, f.name) for f in dataclasses.fields(self))
+
     def c(self, q_stride: int = 0, kv_stride: int = 0) -> cobs_paged_params:
         """The C struct (a copy), with dense token rows unless told otherwise."""
         cp = cobs_paged_params.from_buffer_copy(self._struct)

@@ -139,10 +139,11 @@ cobs_status validate_paged(const cobs_paged_params* p) {
     if (p->dtype != COBS_F32 && p->dtype != COBS_BF16) return fail(COBS_ERR_INVALID_ARG, "dtype %d", p->dtype);
     // slots, positions and (page, head) rows are int32
     if ((long long)p->n_pages * p->page > INT32_MAX || (long long)p->n_pages * p->Hkv > INT32_MAX ||
-        (long long)p->max_pages * p->page > INT32_MAX || (long long)p->n_tokens * p->Hq > INT32_MAX ||
-        ((long long)p->max_pages * p->page / 64 + 16) * p->Hkv > INT32_MAX)  // (tiles of one row tile over all heads)
+        (long long)p->max_pages * p->page > cobs::kMaxKeys || p->n_tokens > cobs::kMaxKeys ||
+        (long long)p->n_tokens * p->Hq > INT32_MAX || ((long long)p->max_pages * p->page / 64 + 16) * p->Hkv > INT32_MAX)  // (tiles of one row tile over all heads)
         return fail(COBS_ERR_UNSUPPORTED,
-                    "n_pages * page, n_pages * Hkv, max_pages * page * Hkv / 64 or n_tokens * Hq exceeds 2^31 - 1");
+                    "n_pages * page, n_pages * Hkv, max_pages * page * Hkv / 64 or n_tokens * Hq exceeds 2^31 - 1, or "
+                    "max_pages * page or n_tokens exceeds 2^30");
     const long long e = p->dtype == COBS_BF16 ? 2 : 4;
     const long long qs = p->q_stride, ks = p->kv_stride;
     if ((qs != 0 && qs < (long long)p->Hq * p->d) || (ks != 0 && ks < (long long)p->Hkv * p->d) || qs * e % 16 != 0 ||

@@ -26,6 +26,7 @@ struct OncePerDevice {
     }
 };
 
+constexpr int kMaxKeys = 1 << 30;    // keys of a request, and token rows
 constexpr int kMaxRequests = 16384;  // the kernels keep one int per request in shared memory
 
 struct PagedDims {
@@ -45,7 +46,10 @@ inline PagedDims make_paged_dims(const cobs_paged_params& p) {
     m.page_shift = 0;
     while ((1 << m.page_shift) < p.page) ++m.page_shift;
     m.n_pages = p.n_pages; m.max_pages = p.max_pages; m.n_tokens = p.n_tokens; m.max_new = p.max_new;
-    m.W = p.window; m.S = p.sinks; m.dtype = p.dtype;
+    // positions are below 2^30: longer windows are no windows, and sums of both stay in 32 bits
+    m.W = p.window < kMaxKeys ? p.window : kMaxKeys;
+    m.S = p.sinks < kMaxKeys ? p.sinks : kMaxKeys;
+    m.dtype = p.dtype;
     m.q_stride = p.q_stride ? p.q_stride : (long long)p.Hq * p.d;
     m.kv_stride = p.kv_stride ? p.kv_stride : (long long)p.Hkv * p.d;
     return m;

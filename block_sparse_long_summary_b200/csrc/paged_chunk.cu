@@ -7,10 +7,9 @@
 // rows are two MMA tiles of 128: each holds floor(128 / G) tokens x the G heads of the group, so K
 // and V are read once per group and a tile spans few positions. Per key tile and row tile g:
 //   S_g = Q_g K^T           tcgen05.mma, M 128, N 128, K d, into 128 TMEM columns
-//   p = 2^(s c - m)         two threads per row (a warp alone on its scheduler waits for its own
-//                           instructions: with one thread per row a pair of tiles took 4.2k cycles, now X);
-//                           m moves only when a row's maximum grows by more than 2^8 (then the
-//                           thread rescales its row of O, which is seldom)
+//   p = 2^(s c - m)         two threads per row, which exchange their maxima; m moves only when a row's
+//                           maximum grows by more than 2^8 (then the threads rescale their row of
+//                           O, which is seldom)
 //   O_g += P_g V            P in bf16 over S's columns (A operand from TMEM), V MN-major
 // The two row tiles alternate: while the tensor pipe runs P V of one and the next Q K^T of it, the
 // other one's softmax runs. MMAs are issued by one thread in the order PV_0(k) QK_0(k+1) PV_1(k)
@@ -18,13 +17,23 @@
 // O_g is up to date, and no barrier is needed for either. A unit of one row tile (single tokens,
 // short chunks) gives both halves of the machine to it: the two groups take its key tiles in turn,
 // each with an accumulator and maxima of its own, joined at the unit's end.
-// Roles: warps 0-15 softmax and epilogue (four for each row tile and half of the columns); warp 16 loads (one TMA box per
-// page and 64 columns; pages no row needs come as out-of-range boxes, that is zeros); warp 17 issues
-// the MMAs; warps 18 and 19 (the first also loads Q) prepare V of the tiles that some row does not see in full: rows of V no
-// row of the unit sees (slots behind the keys, keys before the window: any bits) are set to zero,
-// since 0 * NaN would reach O, and the others are looked over for infinities and NaN: such a tile's
-// product is formed by the softmax threads, key by key, so that only the rows that see them change.
+// Roles: warps 0-15 softmax and epilogue (four for each row tile and half of the columns); warp 16 loads
+// K and V (one TMA box per page and 64 columns; pages no row needs come as out-of-range boxes, that is
+// zeros); warp 17 issues the MMAs; warps 18 and 19 (the first also loads Q) prepare V of the tiles that
+// some row does not see in full: rows of V no row of the unit sees (slots behind the keys, keys before
+// the window: any bits) are set to zero, since 0 * NaN would reach O, and the others are looked over
+// for infinities and NaN: such a tile's product is formed by the softmax threads, key by key, so that
+// only the rows that see them change.
 // Every wait is bounded; one that gives up sets the device error flag and the CTA winds down.
+//
+// What bounds it: the chain of a row tile. 2048 tokens at 32k keys, 64 / 4 heads of 128: 1.92 ms, 1112
+// TFLOP/s, 0.67 of the measured bf16 peak; a pair of key tiles takes some 3.9k cycles, of which the tensor pipe
+// has work for 2.1k and the special-function unit for 2.05k. In a trace a row tile's P V and Q K^T take
+// 1.6k cycles with their hand-over, its softmax 2.2k (maxima 0.4k, powers 1.5k), and two row tiles are
+// all that tensor memory holds (two S of 128 columns, two O of d). Measured and left out: key tiles in
+// halves with N = 64 (four streams, but Q K^T is then bound by shared memory: half as fast); powers partly
+// on the FMA pipes (7% slower and more); P handed over in halves (3%); scores kept in registers between
+// maxima and powers (spills), or read 16 at a time (18%).
 #include <algorithm>
 
 #include "paged.h"
@@ -105,18 +114,23 @@ __device__ __forceinline__ float ld1(uint32_t taddr) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(taddr));
     return v;
 }
-template <int N> __device__ __forceinline__ void rows_sync(int id) { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory"); }
+template <int N> __device__ __forceinline__ void rows_sync(int id) {
+    __syncwarp();  // (the barrier is for converged warps)
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
+}
 // shared memory to global, both 16-byte aligned, a multiple of 16 bytes
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
 }
 
 // Bounded wait without a suspend hint: with one, a poll of a phase that is already complete costs 46
-// cycles, without 15 (clock64 around completed phases), and most waits here find theirs complete.
+// cycles, without 15 (clock64 around completed phases), and most waits here find theirs complete. A poll
+// of an incomplete one comes back after 4 us: kMaxPolls are a quarter of a second.
+constexpr uint32_t kMaxPolls = 1u << 16;
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err) {
     if (mbar_test(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (uint32_t i = 0; i < kMaxWaitIters; ++i) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kMaxPolls; ++i) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -126,10 +140,14 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err
             : "r"(smem_addr(bar)), "r"(parity)
             : "memory");
         if (done) return true;
-        if (global_ns() - t0 > kWaitLimitNs) break;
     }
     report_error(err, kErrWaitTimeout);
     return false;
+}
+// The same for a whole warp, which goes on together: what follows (tcgen05 loads, named barriers) is for
+// converged warps, and the lanes leave the loop above one by one.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* err) {
+    return __all_sync(kFull, wait_on(bar, parity, err));
 }
 
 // n ones from bit 0 up (none for n <= 0, all for n >= 32)
@@ -280,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 const uint32_t fix = nFix;
                 nFix += masked;
                 if (pair && ((k - t0) & 1) != g) continue;
-                if (ok) ok = wait_on(&barS[g], nS & 1, a.err);
+                if (ok) ok = wait_warp(&barS[g], nS & 1, a.err);
                 ++nS;
                 int dirty = 0;  // the stage of V (from 1) where this thread forms the product
                 tc::fence_after_sync();
@@ -332,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     if (grow) m = mt;
                     const float neg = m == -INFINITY ? 0.0f : -m;
                     if (masked && ok) {  // (after S: the tiles before this one have then been prepared)
-                        ok = wait_on(&barFix[fix % kFixDepth], (fix / kFixDepth) & 1, a.err);
+                        ok = wait_warp(&barFix[fix % kFixDepth], (fix / kFixDepth) & 1, a.err);
                         dirty = max(dirty_sh[fix % kFixDepth][0], dirty_sh[fix % kFixDepth][1]);
                     }
                     // p = 2^(s c - m) of 32 keys at a time; P, half as wide, over this half's own scores
@@ -401,13 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             }
             const bool any = kg < t1;  // (a pair's second group may have no tile)
             if (any) {
-                if (ok) ok = wait_on(&barO[g], nO & 1, a.err);
+                if (ok) ok = wait_warp(&barO[g], nO & 1, a.err);
                 ++nO;
             }
             at.advance(2 * (t1 - t0));  // the output's first stage
             const Pos<C::kStages> mine = at.plus(pair ? 0 : g);
             at.advance(sh.stages);
-            if (ok && sh.staged) ok = wait_on(&barKV[mine.s], mine.ph, a.err);
+            if (ok && sh.staged) ok = wait_warp(&barKV[mine.s], mine.ph, a.err);
             tc::fence_after_sync();
             // The threads of one row are in warps of the same TMEM lanes: two of each group, each with a share
             // of the columns, of both accumulators if the unit's tiles went to both groups.
@@ -445,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll 1
                     for (int c = c0; c < c1; c += 32) {
                         float o[32];
+                        __syncwarp();  // (rows of no token have skipped the stores)
                         ld32_to((both ? tmem + lanes + kColO : tO) + c, o);
                         wait_ld32(o);
 #pragma unroll
@@ -543,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     const uint32_t zt = __shfl_sync(kFull, z, ((k - k0) << shift) + (lane & (ppt - 1)));
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++n, at = at.plus(1)) {
-                        if (ok) ok = wait_on(&barFree[at.s], at.ph ^ 1, a.err);
+                        if (ok) ok = wait_warp(&barFree[at.s], at.ph ^ 1, a.err);
                         if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(&barKV[at.s], C::kTile);
                         __syncwarp();
@@ -556,13 +575,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     }
                 }
                 for (uint32_t i = Shape<kKT>(a, w, TM).stages; i > 0 && ok; --i, ++n, at = at.plus(1)) {  // the output's
-                    ok = wait_on(&barFree[at.s], at.ph ^ 1, a.err);
+                    ok = wait_warp(&barFree[at.s], at.ph ^ 1, a.err);
                     if (ok && lane == 0) mbar_arrive(&barKV[at.s]);
                 }
             }
             // wait for the copies that no one consumed (only after a wait that gave up)
             if (!ok)
-                for (uint32_t s = 0; s < C::kStages && s < n; ++s) wait_on(&barKV[s], ((n - 1 - s) / C::kStages) & 1, a.err);
+                for (uint32_t s = 0; s < C::kStages && s < n; ++s) wait_warp(&barKV[s], ((n - 1 - s) / C::kStages) & 1, a.err);
         } else if (warp == kMmaWarp) {
             // -------------------------------------------------------- tensor cores (one thread)
             if (lane == 0) {
@@ -662,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 const int hi = e.last_pos();
                 const Shape<kKT> sh(a, w, TM);
                 if (warp == kFixWarp) {
-                    if (u > 0) ok = wait_on(&barQfree, (u - 1) & 1, a.err);
+                    if (u > 0) ok = wait_warp(&barQfree, (u - 1) & 1, a.err);
                     if (ok && lane == 0) {
                         const int tiles = sh.pair ? 1 : 2;
                         mbar_arrive_expect_tx(&barQ, tiles * C::H * a.G * TM * 128);
@@ -674,10 +693,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 }
                 for (int k = w.t0; k < w.t1 && ok; ++k) {
                     const int j0 = e.key_tile(k) * kKT;
-                    ok = wait_on(&barKV[at.s], at.ph, a.err);
+                    ok = wait_warp(&barKV[at.s], at.ph, a.err);
                     if (ok && lane == 0) mbar_arrive(&barFree[at.s]);
                     at = at.plus(1);
-                    if (ok) ok = wait_on(&barKV[at.s], at.ph, a.err);
+                    if (ok) ok = wait_warp(&barKV[at.s], at.ph, a.err);
                     if (!ok) break;
                     if (masked_tile(a, e, j0)) {
                         unsigned char* sV = sKV + (size_t)at.s * C::kTile;
@@ -722,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     at = at.plus(1);
                 }
                 for (uint32_t i = sh.stages; i > 0 && ok; --i, at = at.plus(1)) {
-                    ok = wait_on(&barKV[at.s], at.ph, a.err);
+                    ok = wait_warp(&barKV[at.s], at.ph, a.err);
                     if (ok && lane == 0) mbar_arrive(&barFree[at.s]);
                 }
             }

@@ -352,7 +352,7 @@ typedef struct {
     int32_t d;          /* head dimension, 64 or 128 */
     int32_t page;       /* tokens per page: 16, 32, 64 or 128 */
     int32_t n_pages;    /* pages of the cache (n_pages * page and n_pages * Hkv at most 2^31 - 1) */
-    int32_t max_pages;  /* width of the block table */
+    int32_t max_pages;  /* width of the block table (max_pages * page at most 2^30) */
     int32_t n_tokens;   /* token rows of Q, K, V, O and slot_map (0: the calls on rows do nothing) */
     int32_t max_new;    /* no request has more new tokens than this (1: single-token decoding) */
     int32_t window;     /* 0: every earlier token is visible; W: the last W, the token itself included */
@@ -396,8 +396,8 @@ cobs_status cobs_paged_append(const cobs_paged_params* p, const void* K, const v
  * cu_new[r + 1] - cu_new[r], and
  *   o_h = sum_j p_j v_j / sum_j p_j,  p_j = exp(q_h . k_j / sqrt(d)),
  * over the keys j <= t of the request with window == 0, or t - j < window, or j < sinks. Products
- * and sums are float32 (bf16: p is rounded to bf16 for the product with v, the sum is not); o is
- * rounded once. What a row does not see does not touch it, whatever it holds (slots behind a
+ * and sums are float32 (bf16: for the product with v a p is rounded to bf16, with max_new = 1 to the
+ * sum of two bf16 parts; the sum of the p is not rounded); o is rounded once. What a row does not see does not touch it, whatever it holds (slots behind a
  * request's keys, pages before its window, later tokens of its chunk). A row that sees nothing
  * (t < 0) gives zeros. A visible page outside the cache counts as zero keys and values and is
  * recorded.

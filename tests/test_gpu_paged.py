@@ -1,7 +1,10 @@
 """The paged-cache calls on the GPU: block tables and slot maps against a walk over every token,
 the append against plain indexing (bit for bit), the attention against 64 bits."""
 import dataclasses
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -206,6 +209,14 @@ def test_window_and_sinks(dtype, window, sinks):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_the_longest_windows_are_no_windows(dtype):
+    top = 2 ** 31 - 1
+    for window, sinks in ((top, 0), (top, top), (2 ** 30 + 1, 5), (7, top)):
+        _check([(500, 1), (3, 1), (-1, 1)], 4, 2, 64, 16, dtype=dtype, window=window, sinks=sinks)
+        _check([(500, 40), (-3, 5), (-40, 41), (-200, 300)], 4, 2, 64, 16, dtype=dtype, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_a_long_context_with_few_rows_is_split(dtype):
     _check([(40000, 1)], 4, 1, 128, 64, dtype=dtype)
     _check([(30000, 40)], 4, 1, 64, 16, dtype=dtype)
@@ -340,6 +351,46 @@ def test_repeated_calls_agree_bit_for_bit_and_replay_from_a_graph(dtype, lens):
     a.K[0], a.V[0] = a.K[0][:, :-3], a.V[0][:, :-3]
     graphs[0].replay()
     a.check()
+    assert C.device_error() == 0
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+from paged_common import Batch, cobs
+C = cobs()
+b = Batch(C, [(300, {n}), (77, 1)], 8, 2, 128, 16, dtype={dtype!r}, max_new={n})
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    b.run()
+g.replay()
+b.check()
+assert C.device_error() == 0
+"""
+
+
+@pytest.mark.parametrize("dtype,n", [("bf16", 1), ("bf16", 40), ("f32", 1), ("f32", 40)])
+def test_the_first_call_of_a_process_may_be_a_captured_one(dtype, n):
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(tests), tests=tests, dtype=dtype, n=n)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("lens", [[(2000, 1), (70, 1)], [(900, 90), (70, 1), (0, 200)]])
+def test_two_streams_at_once(lens):
+    """Calls with workspaces of their own may overlap."""
+    C = cobs()
+    bs = [Batch(C, lens, 8, 2, 128, 64, seed=s) for s in range(4)]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for b, s in zip(bs, streams):
+            b.run(stream=s)
+    for b in bs:
+        b.check()
     assert C.device_error() == 0
 
 

@@ -1,6 +1,8 @@
 """Refusals of the paged-cache calls: all on the host, before anything is launched (no GPU needed),
 and the tables' walk that the GPU tests compare with, on hand-made cases."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -35,6 +37,8 @@ def _attn(lib, cp, ptrs=None, ws=1 << 40):
     (dict(page=8), -2), (dict(page=48), -2), (dict(page=256), -2), (dict(n_pages=0), -1), (dict(max_pages=0), -1),
     (dict(n_tokens=-1), -1), (dict(max_new=0), -1), (dict(window=-1), -1), (dict(sinks=-1, window=4), -1),
     (dict(sinks=2), -1), (dict(n_pages=1 << 25), -2), (dict(max_pages=1 << 25), -2), (dict(n_tokens=1 << 28), -2),
+    (dict(max_pages=(1 << 24) + 1), -2), (dict(Hq=1, Hkv=1, n_tokens=(1 << 30) + 1), -2),
+    (dict(Hq=256, Hkv=256, max_pages=1 << 24), -2),
 ])
 def test_bad_params_are_refused(lib, kw, status):
     p = _p(lib, **kw)
@@ -122,6 +126,8 @@ def test_params_of_the_binding(lib):
     assert q.c().max_new == 7 and q.address != p.address and p.c().max_new == 4
     with pytest.raises(dataclasses.FrozenInstanceError):
         p.R = 5
+    for other in (copy.deepcopy(p), copy.copy(p), pickle.loads(pickle.dumps(p))):
+        assert other == p and other.address != p.address and bytes(other.c()) == bytes(p.c())
 
 
 def test_tables_walk_by_hand(lib):
