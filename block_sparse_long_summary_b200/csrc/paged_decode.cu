@@ -300,7 +300,8 @@ cudaError_t run(const PagedDims& m, const PagedArgs& a, const void* Q, const voi
 
 }  // namespace
 
-int paged_decode_rec_rows(const PagedDims& m) { return m.G; }
+// an even number: a row's d + 2 floats are a multiple of 8 bytes, and records start at multiples of 16
+int paged_decode_rec_rows(const PagedDims& m) { return (m.G + 1) & ~1; }
 int paged_decode_workers(const PagedDims&) { return sm_count(); }
 
 cudaError_t launch_paged_decode(const PagedDims& m, const PagedArgs& a, const void* Q, const void* kc, const void* vc,

@@ -193,6 +193,15 @@ def test_group_sizes(dtype, G):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,new", [(1, 1), (3, 1), (7, 1), (9, 1), (3, 5), (7, 40)])
+def test_odd_groups_with_units_cut_at_both_ends_of_a_range(dtype, d, G, new):
+    # more units than workers, of unequal lengths: ranges begin and end inside units, so that workers leave two records
+    rng = random.Random(100 * G + new)
+    _check([(rng.randrange(1, 1500), 1 + rng.randrange(new)) for _ in range(64)], 3 * G, 3, d, 32, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("page", [16, 64, 128])
 @pytest.mark.parametrize("lens", [
     [(0, 2)], [(0, 128)], [(0, 129), (1, 127)], [(100, 300), (5, 0), (0, 17), (513, 2), (0, 1)], [(2000, 200)],

@@ -73,6 +73,22 @@ def test_null_and_misaligned_pointers_are_refused(lib, at, name):
     assert b"aligned" in lib._lib.cobs_last_error()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("max_new", [1, 4, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_records_of_the_workspace_start_at_16_bytes(lib, dtype, max_new, d):
+    def records(size, workers):  # bytes of both records of a worker: behind 32 bytes each, 256-byte aligned in all
+        return (size - -(-32 * workers // 256) * 256) / workers
+
+    # two heads: two rows of d + 2 floats in each of two records of one worker per SM
+    two = lib.paged_workspace_bytes(_p(lib, Hq=2, Hkv=1, d=64, max_new=1))
+    sms = next(n for n in range(1, 1024) if records(two, n) == 2 * 2 * 66 * 4)
+    for G in range(1, 17):
+        size = lib.paged_workspace_bytes(_p(lib, Hq=G, Hkv=1, d=d, max_new=max_new, dtype=dtype))
+        both = [records(size, k * sms) for k in (1, 2, 3)]  # float32 chunks have two or three workers per SM
+        assert any(b % (2 * 16) == 0 and b >= 2 * 4 * G * (d + 2) for b in both), (G, size, both)
+
+
 def test_small_workspace_is_refused(lib):
     p = _p(lib)
     need = lib.paged_workspace_bytes(p)
