@@ -197,7 +197,7 @@ def test_group_sizes(dtype, G):
 def test_odd_groups_with_units_cut_at_both_ends_of_a_range(dtype, d, G, new):
     # more units than workers, of unequal lengths: ranges begin and end inside units, so that workers leave two records
     rng = random.Random(100 * G + new)
-    _check([(rng.randrange(1, 1500), 1 + rng.randrange(new)) for _ in range(64)], 3 * G, 3, d, 32, dtype)
+    _check([(rng.randrange(1, 1500), 1 + rng.randrange(new)) for _ in range(64)], 3 * G, 3, d, 32, dtype=dtype)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
