@@ -34,6 +34,8 @@
 // halves with N = 64 (four streams, but Q K^T is then bound by shared memory: half as fast); powers partly
 // on the FMA pipes (7% slower and more); P handed over in halves (3%); scores kept in registers between
 // maxima and powers (spills), or read 16 at a time (18%).
+#include <stddef.h>
+
 #include <algorithm>
 
 #include "paged.h"
@@ -123,6 +125,13 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
 }
 
+// a box of shared memory (128-byte swizzle) to a 3-D tensor
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y), "r"(z),
+                 "r"(smem_addr(src))
+                 : "memory");
+}
+
 // Bounded wait without a suspend hint: with one, a poll of a phase that is already complete costs 46
 // cycles, without 15 (clock64 around completed phases), and most waits here find theirs complete. A poll
 // of an incomplete one comes back after 4 us: kMaxPolls are a quarter of a second.
@@ -188,23 +197,44 @@ struct Pos {
 };
 
 // How a unit runs: one row tile whose key tiles the two groups take in turn, or two; and whether its
-// output leaves through the ring (a stage per row tile, rows written to shared memory and copied out in
-// bulk): a thread's row is 2 d bytes apart from its neighbour's, so direct stores of 32 rows touch 32
-// lines each, which took 7k cycles per unit of 256 rows against 1k through the ring. One warp's rows and
-// records go directly.
+// output leaves through the ring (a stage per row tile): a thread's row is 2 d bytes apart from its
+// neighbour's, so direct stores of 32 rows touch 32 lines each, which took 7k cycles per unit of 256 rows
+// against 1k through the ring. A full row tile leaves as one box per 64 columns (a copy per token is issued
+// lane by lane: 3 to 4k cycles for 32 of them), a partial one token by token. One warp's rows and records go
+// directly.
 template <int KT>
 struct Shape {
     bool pair, staged;
     uint32_t stages;  // of the output
-    __device__ __forceinline__ Shape(const PagedArgs& a, const PagedWalk<KT>& w, int TM) {
-        pair = w.e.n <= TM;
-        staged = w.whole() && w.e.n * a.G > 32;
+    __device__ __forceinline__ Shape(const PagedArgs& a, int n, bool whole, int TM) {
+        pair = n <= TM;
+        staged = whole && n * a.G > 32;
         stages = staged ? (pair ? 1 : 2) : 0;
     }
+    __device__ __forceinline__ Shape(const PagedArgs& a, const PagedWalk<KT>& w, int TM) : Shape(a, w.e.n, w.whole(), TM) {}
 };
 
+// A walk in one register of a warp: value k in lane k.
+template <int KT>
+__device__ __forceinline__ int pack_walk(const PagedWalk<KT>& w, int lane) {
+    static_assert(sizeof(PagedWalk<KT>) == 17 * sizeof(int), "17 values");
+    const int* f = reinterpret_cast<const int*>(&w);
+    int v = 0;
+#pragma unroll
+    for (int k = 0; k < 17; ++k) v = lane == k ? f[k] : v;
+    return v;
+}
+template <int KT>
+__device__ __forceinline__ PagedWalk<KT> unpack_walk(int v) {
+    PagedWalk<KT> w;
+    int* f = reinterpret_cast<int*>(&w);
+#pragma unroll
+    for (int k = 0; k < 17; ++k) f[k] = __shfl_sync(kFull, v, k);
+    return w;
+}
+
 struct ChunkMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
 };
 
 // A tile some row of the unit does not see in full.
@@ -277,14 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         uint32_t nS = 0, nO = 0, nFix = 0;
         Pos<C::kStages> at;  // of the unit's first tile
         int piece = 0;
-        // The walk lies in local memory behind a pointer the compiler cannot see through: of its 17 registers
-        // the loop over the tiles needs six, and left to itself the compiler spilled in that loop.
-        PagedWalk<kKT>* pw = &w;
-        asm volatile("" : "+l"(pw)::"memory");
-        for (; more; more = pw->next(a, TQ), ++piece) {
-            const int pos0 = pw->e.pos0, en = pw->e.n, t0 = pw->t0, t1 = pw->t1, sT = pw->e.sT, loT = pw->e.loT;
-            const Shape<kKT> sh(a, *pw, TM);
-            const bool pair = sh.pair;
+        // Of the walk's 17 values the loop over the tiles needs six. The others wait in one register, value k in
+        // lane k (as registers of every lane they were spilled in that loop, and in local memory they did not fit
+        // beside the other threads' in what the shared memory leaves of L1: 1.6k cycles per unit).
+        int packed = pack_walk(w, lane);
+#define PACKED(field) __shfl_sync(kFull, packed, offsetof(PagedWalk<kKT>, field) / sizeof(int))
+        for (; more; ++piece) {
+            const int pos0 = PACKED(e.pos0), en = PACKED(e.n), t0 = PACKED(t0), t1 = PACKED(t1), sT = PACKED(e.sT), loT = PACKED(e.loT);
+            const bool pair = en <= TM;
             const int tok0 = pair ? 0 : g * TM;       // first token of this group's rows
             const int ntok = min(TM, en - tok0);
             const bool live = tok < ntok;
@@ -422,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 if (ok) ok = wait_warp(&barO[g], nO & 1, a.err);
                 ++nO;
             }
+            const bool whole = t0 == 0 && t1 == PACKED(e.nt);
+            const Shape<kKT> sh(a, en, whole, TM);
             at.advance(2 * (t1 - t0));  // the output's first stage
             const Pos<C::kStages> mine = at.plus(pair ? 0 : g);
             at.advance(sh.stages);
@@ -430,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             // The threads of one row are in warps of the same TMEM lanes: two of each group, each with a share
             // of the columns, of both accumulators if the unit's tiles went to both groups.
             float f0 = 1.0f, f1 = 0.0f;  // factors of O_0 and O_1 (of O_g alone, if not both)
-            const bool both = pair && t1 - t0 > 1, empty = t < 0, whole = pw->whole();
+            const bool both = pair && t1 - t0 > 1, empty = t < 0;
             if (warp_live && any) {
                 auto meet = [&] { if (both) rows_sync<128>(9 + (warp & 3)); else rows_sync<64>(1 + 4 * g + (warp & 3)); };
                 row_sh[g][half][row] = l;
@@ -450,14 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                 }
                 meet();  // before the slots are written again
                 const int c0 = both ? 32 * (2 * g + half) : half * (D / 2), c1 = both ? min(c0 + 32, D) : c0 + D / 2;
-                const size_t orow = (size_t)(pw->e.row0 + tok0 + (live ? tok : 0)) * a.Hq + pw->h * a.G + (live ? hrow : 0);
+                const size_t orow = (size_t)(PACKED(e.row0) + tok0 + (live ? tok : 0)) * a.Hq + PACKED(h) * a.G + (live ? hrow : 0);
                 float* rec = a.rec + ((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * a.rec_rows * (D + 2);
+                const bool full = ntok == TM;  // a staged tile leaves as swizzled boxes
                 const int rrow = live ? (tok0 + tok) * a.G + hrow : 0;
-                unsigned char* out = sh.staged ? sKV + (size_t)mine.s * C::kTile + row * (2 * D)
+                unsigned char* out = sh.staged ? sKV + (size_t)mine.s * C::kTile + row * (full ? 128 : 2 * D)
                                                : reinterpret_cast<unsigned char*>(static_cast<__nv_bfloat16*>(a.O) + orow * D);
                 if (whole) {
-                    f0 = empty ? 0.0f : f0 / l;
-                    f1 = empty ? 0.0f : f1 / l;
+                    const float inv = empty ? 0.0f : __fdividef(1.0f, l);  // (2 units in the last place; the result has 8 bits)
+                    f0 *= inv;
+                    f1 *= inv;
                 }
                 {
 #pragma unroll 1
@@ -481,7 +515,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                             for (int j = 0; j < 4; ++j)
                                 v[j] = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
                                                   pack_bf16(o[8 * j + 4], o[8 * j + 5]), pack_bf16(o[8 * j + 6], o[8 * j + 7]));
-                            if (sh.staged) {
+                            if (sh.staged && full) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    *reinterpret_cast<uint4*>(out + (c >> 6) * kBox + (((((c & 63) >> 3) + j) ^ (row & 7)) << 4)) = v[j];
+                            } else if (sh.staged) {
                                 // the rows' common pitch puts a chunk of all rows in the same banks: lane r
                                 // writes chunk (j + r) % 4 in step j, two steps of exchange
                                 const bool r1 = lane & 1, r2 = lane & 2;
@@ -514,23 +552,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             }
             // neither group's accumulator is written again before both have read it
             tc::fence_before_sync();
+            const bool copier = sh.staged && (warp & 3) == 0 && half == 0 && (!pair || g == 0);
             if (sh.staged) {
                 fence_proxy_async();
                 if (pair) rows_sync<512>(15); else rows_sync<256>(13 + g);
-                if ((warp & 3) == 0 && half == 0 && (!pair || g == 0)) {  // a token's rows of the group are one run of both memories
+                if (copier) {
                     const unsigned char* src = sKV + (size_t)mine.s * C::kTile;
-                    for (int i = lane; i < ntok; i += 32)
-                        bulk_s2g(static_cast<__nv_bfloat16*>(a.O) + ((size_t)(pw->e.row0 + tok0 + i) * a.Hq + pw->h * a.G) * D,
-                                 src + (size_t)i * a.G * 2 * D, a.G * 2 * D);
+                    const int row0 = PACKED(e.row0) + tok0, head = PACKED(h) * a.G;
+                    if (ntok == TM) {
+                        if (lane == 0)
+                            for (int h = 0; h < C::H; ++h)
+                                tma_store_3d(&maps.o, 64 * h, head, row0, src + h * kBox);
+                    } else {  // (a box would write the next request's rows) a token's rows are one run of both memories
+                        for (int i = lane; i < ntok; i += 32)
+                            bulk_s2g(static_cast<__nv_bfloat16*>(a.O) + ((size_t)(row0 + i) * a.Hq + head) * D,
+                                     src + (size_t)i * a.G * 2 * D, a.G * 2 * D);
+                    }
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&barFree[mine.s]);
                 }
             } else if (both && warp_live) {
                 rows_sync<128>(9 + (warp & 3));
             }
+            {
+                PagedWalk<kKT> x = unpack_walk<kKT>(packed);
+                more = x.next(a, TQ);
+                packed = pack_walk(x, lane);
+            }
+            if (copier) {
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&barFree[mine.s]);
+            }
         }
+#undef PACKED
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
         if (warp == kLoadWarp) {
@@ -760,12 +814,13 @@ cudaError_t run(const PagedDims& m, const PagedArgs& a, const void* Q, const voi
     static_assert((kMaxRequests + 1) * 4 <= C::kStages * C::kTile, "the plan's scratch");
     const int TM = 128 / m.G, workers = sm_count();
     ChunkMaps maps;
-    const uint64_t qd[3] = {(uint64_t)D, (uint64_t)m.Hq, (uint64_t)m.n_tokens}, qs[2] = {(uint64_t)D * 2, (uint64_t)m.q_stride * 2};
+    const uint64_t qd[3] = {(uint64_t)D, (uint64_t)m.Hq, (uint64_t)m.n_tokens}, qs[2] = {(uint64_t)D * 2, (uint64_t)m.q_stride * 2},
+                   os[2] = {(uint64_t)D * 2, (uint64_t)m.Hq * D * 2};
     const uint32_t qb[3] = {64, (uint32_t)m.G, (uint32_t)TM};
     const uint64_t cd[3] = {(uint64_t)D, (uint64_t)m.page, (uint64_t)m.n_pages * m.Hkv}, cs[2] = {(uint64_t)D * 2, (uint64_t)m.page * D * 2};
     const uint32_t cb[3] = {64, (uint32_t)m.page, 1};
     if (!encode_tmap_bf16_3d(&maps.q, Q, qd, qs, qb) || !encode_tmap_bf16_3d(&maps.k, kc, cd, cs, cb) ||
-        !encode_tmap_bf16_3d(&maps.v, vc, cd, cs, cb))
+        !encode_tmap_bf16_3d(&maps.v, vc, cd, cs, cb) || !encode_tmap_bf16_3d(&maps.o, a.O, qd, os, qb))
         return cudaErrorInvalidValue;
     static OncePerDevice once;
     cudaError_t e = once.run([] { return cudaFuncSetAttribute(paged_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem); });
