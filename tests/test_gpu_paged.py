@@ -239,6 +239,12 @@ def test_many_requests(dtype):
     _check([(int(2 ** rng.uniform(0, 9)), rng.choice([0, 1, 1, 1, 5, 60])) for _ in range(600)], 2, 1, 64, 16, dtype=dtype)
 
 
+@pytest.mark.parametrize("new", [1, 3])
+def test_attention_at_the_largest_request_count(new):
+    rng = random.Random(3)
+    _check([(rng.randrange(40), rng.randrange(1, new + 1)) for _ in range(16384)], 1, 1, 64, 16)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_large_scores_keep_the_running_maximum(dtype):
     _check([(3000, 3), (500, 200)], 4, 2, 128, 64, dtype=dtype, scale=4.0)
