@@ -43,6 +43,14 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 
+// The two parts of p >= 0 (see the use): the upper 16 bits of two, packed, and what they leave.
+__device__ __forceinline__ uint32_t high_parts(float x, float y) {
+    return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+}
+__device__ __forceinline__ float low_part(float x) {
+    return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), 1.17549435e-38f);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kT, 1) paged_decode_kernel(PagedArgs a, const __nv_bfloat16* Q, long long q_stride,
                                                              const __nv_bfloat16* kc, const __nv_bfloat16* vc) {
@@ -197,8 +205,11 @@ __global__ void __launch_bounds__(kT, 1) paged_decode_kernel(PagedArgs a, const 
                                 }
                             }
                 }
-                // p in two bf16 parts: its rounding is then 2^-17, next to nothing beside o's (with one part the
-                // error against 64 bits was 1.4 times that of o's rounding; the time is the same)
+                // p in two bf16 parts, the first one cut to 8 bits and the second (under 2^-7 of p) rounded: p is off by
+                // 2^-15, next to nothing beside o's rounding (with one part the error against 64 bits was 1.4 times that
+                // of o's rounding; the time is the same). Neither part of a visible key's p is negative, and the second
+                // is at least 2^-126, the smallest normal: an infinite value then gives that infinity in both products,
+                // where a second part of 0 or below would make it NaN. (A hidden key's value is zero in the ring.)
                 uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -207,11 +218,10 @@ __global__ void __launch_bounds__(kT, 1) paged_decode_kernel(PagedArgs a, const 
                     const float p2 = exp2_fast(s[n][2] - u0), p3 = exp2_fast(s[n][3] - u1);
                     l[n][0] += p0 + p2;
                     l[n][1] += p1 + p3;
-                    const uint32_t a0 = pack_bf16(p0, p1), a1 = pack_bf16(p2, p3);
-                    pb[n][0] = movmatrix_trans(a0);
-                    pb[n][1] = movmatrix_trans(a1);
-                    pl[n][0] = movmatrix_trans(pack_bf16(p0 - __uint_as_float(a0 << 16), p1 - __uint_as_float(a0 & 0xffff0000u)));
-                    pl[n][1] = movmatrix_trans(pack_bf16(p2 - __uint_as_float(a1 << 16), p3 - __uint_as_float(a1 & 0xffff0000u)));
+                    pb[n][0] = movmatrix_trans(high_parts(p0, p1));
+                    pb[n][1] = movmatrix_trans(high_parts(p2, p3));
+                    pl[n][0] = movmatrix_trans(pack_bf16(low_part(p0), low_part(p1)));
+                    pl[n][1] = movmatrix_trans(pack_bf16(low_part(p2), low_part(p3)));
                 }
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t) {

@@ -1,0 +1,34 @@
+"""Values and table entries at the edges of the paged attention: infinities and NaN in V, also where a row
+has one key only."""
+import pytest
+import torch
+
+from paged_common import Batch, cobs
+
+pytestmark = pytest.mark.gpu
+
+
+def _put(b, r, t, value, columns=slice(None, None, 7)):
+    """V of token t of request r holds `value` in some columns of every head."""
+    page = b.p.page
+    b.V[r][:, t, columns] = value
+    b.v_cache[b.table[r, t // page].item(), :, t % page] = b.V[r][:, t].to(b.v_cache.device)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("G,d,page", [(1, 128, 16), (4, 128, 64), (8, 64, 32), (11, 64, 128), (16, 128, 16)])
+def test_values_of_single_tokens(dtype, value, G, d, page):
+    """A visible infinity reaches the output as what it is (its weight is a positive number), a hidden one
+    does not, and the other columns keep their accuracy."""
+    C = cobs()
+    lens = [(0, 1), (1, 1), (100, 1), (130, 1), (3000, 1)]
+    for W, S in ((0, 0), (40, 3)):
+        b = Batch(C, lens, 2 * G, 2, d, page, dtype=dtype, window=W, sinks=S, drop_unseen=False, seed=G)
+        for r, t in ((0, 0), (1, 1), (2, 60), (2, 99), (3, 2), (4, 5), (4, 2990)):
+            _put(b, r, t, value)
+        _put(b, 4, 2999, -value, slice(3, None, 14))
+        C.device_error(reset=True)
+        b.run()
+        assert C.device_error() == 0
+        b.check((W, S))
