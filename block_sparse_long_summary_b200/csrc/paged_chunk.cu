@@ -597,21 +597,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             for (; more && ok; more = w.next(a, TQ)) {
                 const PagedEntry& e = w.e;
                 const int hi = e.last_pos();
-                auto entry = [&](int k) {  // raw table entry of this lane's page of the look-up from tile k
+                int raw, k0 = w.t0;
+                bool needed;
+                auto look_up = [&](int k) {  // table entry (any value) of this lane's page of the tiles from k on
                     const int j = k + my_tile < w.t1 ? e.key_tile(k + my_tile) * kKT + my_key : INT_MAX;
-                    return j <= hi && (j >> a.page_shift) < a.max_pages && (j + a.page > e.lo || j < a.S)
-                               ? __ldg(a.table + (size_t)e.r * a.max_pages + (j >> a.page_shift)) : INT_MIN;
+                    needed = j <= hi && (j >> a.page_shift) < a.max_pages && (j + a.page > e.lo || j < a.S);
+                    raw = needed ? __ldg(a.table + (size_t)e.r * a.max_pages + (j >> a.page_shift)) : -1;
                 };
-                int raw = entry(w.t0), k0 = w.t0;
+                look_up(w.t0);
                 uint32_t z = 0;
                 for (int k = w.t0; k < w.t1 && ok; ++k) {
                     if (k == w.t0 || k == k0 + per) {
                         k0 = k;
                         // pages no row needs, and (recorded) those outside the cache, read as zeros
                         const bool in = raw >= 0 && raw < a.n_pages;
-                        if (!in && raw != INT_MIN) report_error(a.err, kErrBadIndex);
+                        if (!in && needed) report_error(a.err, kErrBadIndex);
                         z = in ? (uint32_t)raw * a.Hkv + w.h : zero_box;
-                        raw = entry(k0 + per);
+                        look_up(k0 + per);
                     }
                     const uint32_t zt = __shfl_sync(kFull, z, ((k - k0) << shift) + (lane & (ppt - 1)));
 #pragma unroll

@@ -70,16 +70,16 @@ __global__ void __launch_bounds__(kT, 1) paged_decode_kernel(PagedArgs a, const 
     if (tid == 0) a.seg[blockIdx.x] = w.seg(a, start.range, blockIdx.x);
     bool fetching = more;
     int ft = f.t0;          // tile to look up next
-    int page = -1, j = 0;   // page and first key of the slice looked up last (-1: nothing to copy)
-    bool looked = false;
+    int page = -1, j = 0;   // table entry (any value) and first key of the slice looked up last
+    bool looked = false;    // whether it is to be copied
     // the table entry of the next slice: asked for a tile before it is used
     auto look_up = [&] {
-        looked = fetching;
+        looked = false;
         if (!fetching) return;
         const int pos = f.e.pos0;
         j = f.e.key_tile(ft) * kKT + warp * kSlice;
-        const bool any = j <= pos && (j + kSlice > f.e.lo || j < a.S) && (j >> a.page_shift) < a.max_pages;
-        page = any ? __ldg(a.table + (size_t)f.e.r * a.max_pages + (j >> a.page_shift)) : INT_MIN;
+        looked = j <= pos && (j + kSlice > f.e.lo || j < a.S) && (j >> a.page_shift) < a.max_pages;
+        if (looked) page = __ldg(a.table + (size_t)f.e.r * a.max_pages + (j >> a.page_shift));
     };
     auto advance = [&] {
         if (fetching && ++ft == f.t1) {
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kT, 1) paged_decode_kernel(PagedArgs a, const 
     uint32_t put = 0;  // stage
     const uint32_t lane_row = lane / (D / 8), lane_col = lane % (D / 8);
     auto fetch = [&] {  // the slice looked up, into the next stage
-        if (looked && page != INT_MIN) {
+        if (looked) {
             const bool in = page >= 0 && page < a.n_pages;
             if (!in && lane == 0) report_error(a.err, kErrBadIndex);
             const int pos = f.e.pos0, off = j & (a.page - 1);

@@ -49,23 +49,23 @@ struct Slices {
     const PagedArgs& a;
     const float *kc, *vc;
     PagedWalk<kKT> f;    // the unit whose slices are being copied
-    bool fetching, looked;
+    bool fetching, looked;  // looked: the slice looked up last is to be copied
     int tile;               // to look up next
-    int page, j;            // page (INT_MIN: nothing to copy) and first key of the slice looked up last
+    int page, j;            // table entry (any value) and first key of the slice looked up last
     uint32_t ring, put;     // this warp's ring, next stage
     int warp, lane;
 
     __device__ __forceinline__ Slices(const PagedArgs& a_, const float* k, const float* v, const PagedStart<kKT>& s, uint32_t ring_)
-        : a(a_), kc(k), vc(v), f(s.walk), fetching(s.more), looked(false), tile(s.walk.t0), page(INT_MIN), j(0), ring(ring_), put(0),
+        : a(a_), kc(k), vc(v), f(s.walk), fetching(s.more), looked(false), tile(s.walk.t0), page(-1), j(0), ring(ring_), put(0),
           warp(threadIdx.x >> 5), lane(threadIdx.x & 31) {}
     // the table entry of the next slice: asked for a tile before it is used
     __device__ __forceinline__ void look_up() {
-        looked = fetching;
+        looked = false;
         if (!fetching) return;
         const int pos = f.e.pos0;
         j = f.e.key_tile(tile) * kKT + warp * kSlice;
-        const bool any = j <= pos && (j + kSlice > f.e.lo || j < a.S) && (j >> a.page_shift) < a.max_pages;
-        page = any ? __ldg(a.table + (size_t)f.e.r * a.max_pages + (j >> a.page_shift)) : INT_MIN;
+        looked = j <= pos && (j + kSlice > f.e.lo || j < a.S) && (j >> a.page_shift) < a.max_pages;
+        if (looked) page = __ldg(a.table + (size_t)f.e.r * a.max_pages + (j >> a.page_shift));
     }
     __device__ __forceinline__ void advance() {
         if (fetching && ++tile == f.t1) {
@@ -76,7 +76,7 @@ struct Slices {
     // The slice looked up, into the next stage: whole rows, the 16-byte chunks of odd rows in the other half of
     // each 128 bytes (two rows are read at once); rows the token does not see are zero.
     __device__ __forceinline__ void fetch() {
-        if (looked && page != INT_MIN) {
+        if (looked) {
             const bool in = page >= 0 && page < a.n_pages;
             if (!in && lane == 0) report_error(a.err, kErrBadIndex);
             constexpr int kChunks = D / 4, kRows = 32 / kChunks;  // 16-byte chunks of a row, rows a warp copies at once

@@ -32,3 +32,28 @@ def test_values_of_single_tokens(dtype, value, G, d, page):
         b.run()
         assert C.device_error() == 0
         b.check((W, S))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("entry", [-1, -2, -2 ** 31, -2 ** 31 + 1, 1 << 20, 2 ** 31 - 1])
+@pytest.mark.parametrize("new", [1, 30])
+def test_every_entry_outside_the_cache_counts_as_zeros_and_is_recorded(dtype, entry, new):
+    C = cobs()
+    b = Batch(C, [(3000, new), (90, 1)], 4, 2, 128, 32, dtype=dtype)
+    warm = Batch(C, [(3000, new), (90, 1)], 4, 2, 128, 32, dtype=dtype, seed=1)   # shared memory holds other keys
+    for j in (1, 40, 93):
+        b.table[0, j] = entry
+        b.K[0][:, 32 * j:32 * (j + 1)] = 0
+        b.V[0][:, 32 * j:32 * (j + 1)] = 0
+    C.device_error(reset=True)
+    warm.run()
+    assert C.device_error() == 0
+    b.run()
+    assert C.device_error(reset=True) == 1
+    b.check(entry)
+    # entries of pages that no row sees may be anything
+    b = Batch(C, [(3000, new), (90, 1)], 4, 2, 128, 32, dtype=dtype, window=50, sinks=2)
+    b.table[b.table < 0] = entry
+    b.run()
+    assert C.device_error() == 0
+    b.check(entry)
