@@ -360,7 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     for (int j = 0; j < 32; j += 2) mx[(j >> 1) & 1] = max3(mx[(j >> 1) & 1], s[j], s[j + 1]);
                     const float mine = fmaxf(mx[0], mx[1]);
                     row_sh[g][half][row] = mine;
-                    rows_sync<64>(1 + 4 * g + (warp & 3));  // the warp with the other half of these rows
+                    // the warp with the other half of these rows; its scores stored above may be read below (dirty)
+                    if (masked) tc::fence_before_sync();
+                    rows_sync<64>(1 + 4 * g + (warp & 3));
+                    if (masked) tc::fence_after_sync();
                     const float mt = fmaxf(mine, row_sh[g][half ^ 1][row]) * sl2;
                     const bool grow = mt > m + 8.0f;  // (from -infinity too; never for a row that sees nothing)
                     if (k > kg && __any_sync(kFull, grow && m != -INFINITY)) {
@@ -465,6 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             const bool both = pair && t1 - t0 > 1, empty = t < 0;
             if (warp_live && any) {
                 auto meet = [&] { if (both) rows_sync<128>(9 + (warp & 3)); else rows_sync<64>(1 + 4 * g + (warp & 3)); };
+                // (each group has waited for its own accumulator only, and reads the other's behind the meetings)
+                if (both) tc::fence_before_sync();
                 row_sh[g][half][row] = l;
                 meet();
                 l = row_sh[g][0][row] + row_sh[g][1][row];
@@ -481,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
                     l = l0 * f0 + l1 * f1;
                 }
                 meet();  // before the slots are written again
+                if (both) tc::fence_after_sync();
                 const int c0 = both ? 32 * (2 * g + half) : half * (D / 2), c1 = both ? min(c0 + 32, D) : c0 + D / 2;
                 const size_t orow = (size_t)(PACKED(e.row0) + tok0 + (live ? tok : 0)) * a.Hq + PACKED(h) * a.G + (live ? hrow : 0);
                 float* rec = a.rec + ((size_t)blockIdx.x * 2 + (piece == 0 ? 0 : 1)) * a.rec_rows * (D + 2);

@@ -57,3 +57,23 @@ def test_every_entry_outside_the_cache_counts_as_zeros_and_is_recorded(dtype, en
     b.run()
     assert C.device_error() == 0
     b.check(entry)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[(3000, 20)], [(700, 32), (40, 5)], [(90, 30), (200, 31), (5, 2)]])
+def test_chunks_of_one_row_tile_with_infinite_values(lens, d):
+    """The key tiles of at most 128 rows go to two groups of threads, whose accumulators are joined; tiles with
+    infinities that some rows do not see are multiplied by the threads. Calls agree bit for bit."""
+    C = cobs()
+    b = Batch(C, lens, 8, 2, d, 32, window=600, sinks=5, drop_unseen=False)
+    for r, (c, n) in enumerate(lens):
+        for t in (c + n - 1, c + n // 2, max(0, c - 300), 3):
+            _put(b, r, t, float("inf"), slice(t % 5, None, 11))
+    b.run()
+    b.check()
+    first = b.O.clone()
+    for _ in range(30):
+        b.O.fill_(7.0)
+        b.run()
+        assert torch.equal(b.O.view(torch.int16), first.view(torch.int16))
+    assert C.device_error() == 0
