@@ -221,8 +221,12 @@ __global__ void __launch_bounds__(kT, blocks_per_sm(D, M)) paged_simt_kernel(Pag
 template <int D, int M>
 cudaError_t run(const PagedArgs& a, int workers, const float* Q, long long q_stride, const float* kc, const float* vc,
                 cudaStream_t s) {
-    const size_t smem = std::max(simt_smem<D, M>(), (size_t)(a.R + 1) * sizeof(int));
-    cudaError_t e = cudaFuncSetAttribute(paged_simt_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr auto smem_of = [](int R) { return std::max(simt_smem<D, M>(), (size_t)(R + 1) * sizeof(int)); };
+    const size_t smem = smem_of(a.R);
+    static OncePerDevice once;  // (the largest call's limit: a call's own would be lowered by another thread's)
+    cudaError_t e = once.run([&] {
+        return cudaFuncSetAttribute(paged_simt_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(kMaxRequests));
+    });
     if (e != cudaSuccess) return e;
     paged_simt_kernel<D, M><<<workers, kT, smem, s>>>(a, Q, q_stride, kc, vc);
     e = cudaGetLastError();

@@ -11,6 +11,7 @@ namespace cobs {
 namespace {
 
 constexpr int kTT = 512;
+constexpr int tables_smem(int R) { return (2 * R + 1) * (int)sizeof(int); }
 
 struct TableArgs {
     const int32_t *cached, *fresh, *free_pages, *free_count;
@@ -142,14 +143,14 @@ cudaError_t launch_paged_tables(const PagedDims& m, const int32_t* cached_len, c
     a.table = block_table; a.cu = cu_new; a.kv_len = kv_len; a.slots = slot_map; a.counts = counts; a.err = err;
     a.R = m.R; a.n_free = n_free; a.n_pages = m.n_pages; a.max_pages = m.max_pages; a.page_shift = m.page_shift;
     a.n_tokens = m.n_tokens; a.max_new = m.max_new;
-    const size_t smem = (size_t)(2 * m.R + 1) * sizeof(int);
-    if (smem > 32 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    static OncePerDevice once;  // (the largest call's limit: a call's own would be lowered by another thread's)
+    const cudaError_t e = once.run([] {
+        return cudaFuncSetAttribute(paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tables_smem(kMaxRequests));
+    });
+    if (e != cudaSuccess) return e;
     const int blocks = std::max(1, std::min((m.n_tokens + kTT - 1) / kTT, sm_count()));
     count_launch();
-    paged_tables_kernel<<<blocks, kTT, smem, s>>>(a);
+    paged_tables_kernel<<<blocks, kTT, tables_smem(m.R), s>>>(a);
     return cudaGetLastError();
 }
 
