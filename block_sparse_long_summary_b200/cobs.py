@@ -390,7 +390,16 @@ def _load_binding(path: str = os.path.join(_HERE, "lib", "_paged.so")):
     return module
 
 
-_paged = _load_binding()
+class _Binding:
+    """The native binding of the paged calls, loaded by the first of them: it is built against one version
+    of PyTorch, which the other calls do not depend on."""
+
+    def __getattr__(self, name):
+        vars(self).update((f, getattr(module, f)) for module in [_load_binding()] for f in ("tables", "append", "attn"))
+        return object.__getattribute__(self, name)
+
+
+_paged = _Binding()
 
 
 def paged_workspace_bytes(p: PagedParams) -> int:

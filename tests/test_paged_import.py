@@ -1,0 +1,55 @@
+"""The package without a usable native binding of the paged calls: everything else works, and the paged calls
+say what is missing."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from block_sparse_long_summary_b200 import build as B
+
+REFUSED = """
+import importlib.machinery, os
+real = importlib.machinery.ExtensionFileLoader.create_module
+def create(self, spec):
+    if os.path.basename(self.path).startswith("_paged"):
+        raise ImportError("undefined symbol (built for another PyTorch)")
+    return real(self, spec)
+importlib.machinery.ExtensionFileLoader.create_module = create
+"""
+MISSING = """
+import os
+real = os.path.exists
+os.path.exists = lambda p: not os.path.basename(str(p)).startswith("_paged") and real(p)
+"""
+REST = """
+from block_sparse_long_summary_b200 import cobs
+assert cobs.version() > 0 and cobs.workspace_bytes(cobs.Params(B=1, Hq=4, Hkv=1, d=128, T=4096, topk=8, window=512), cobs.COBS_WS_DECODE) > 0
+p = cobs.PagedParams(R=1, Hq=4, Hkv=1, d=128, page=64, n_pages=4, max_pages=4, n_tokens=1, max_new=1)
+assert cobs.paged_workspace_bytes(p) > 0
+for _ in range(2):
+    try:
+        cobs.cobs_paged_append(p, None, None, None, None, None)
+    except ImportError as e:
+        assert "undefined symbol" in str(e) or "not built" in str(e)
+    else:
+        raise SystemExit("the call went on")
+"""
+
+
+@pytest.mark.parametrize("setup", [REFUSED, MISSING], ids=["refused", "missing"])
+def test_only_the_paged_calls_need_the_binding(setup):
+    B.build()
+    r = subprocess.run([sys.executable, "-c", setup + REST], capture_output=True, text=True, cwd=B.ROOT)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_the_binding_is_loaded_once():
+    B.build()
+    from block_sparse_long_summary_b200 import cobs
+    with pytest.raises(TypeError, match="tensor"):
+        cobs.cobs_paged_append(cobs.PagedParams(R=1, Hq=4, Hkv=1, d=128, page=64, n_pages=4, max_pages=4, n_tokens=1, max_new=1),
+                               None, None, None, None, None)
+    assert vars(cobs._paged)["attn"] is cobs._paged.attn
+    with pytest.raises(AttributeError):
+        cobs._paged.no_such_call
