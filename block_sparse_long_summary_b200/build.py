@@ -1,10 +1,10 @@
 """Build the COBS CUDA library (``lib/libcobs.so``) for sm_100a with nvcc, and the native binding of its
-paged-cache calls (``lib/_paged.so``) with the host compiler.
+paged-cache calls (``lib/_paged-<PyTorch>-<Python>.so``) with the host compiler.
 
 Usage: ``python -m block_sparse_long_summary_b200.build [--force]``.
 The library is built in place (objects under ``_build/``) so that it travels with the
 source tree; it links the CUDA runtime statically and nothing from PyTorch. The binding links the
-library and PyTorch.
+library and PyTorch; its name holds the versions it is built for, so that others get their own.
 """
 from __future__ import annotations
 
@@ -20,7 +20,6 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libcobs.so")
-BINDING = os.path.join(LIB_DIR, "_paged.so")
 BINDING_SRC = "paged_binding.cpp"
 SOURCES = ["api.cu", "summary.cu", "select.cu", "decode.cu", "decode_stream.cu", "decode_step.cu", "tma.cu", "prefill.cu",
            "mass.cu", "basis.cu", "paged_tables.cu", "paged_attn.cu", "paged_simt.cu",
@@ -39,11 +38,16 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _deps_mtime() -> float:
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS if os.path.exists(os.path.join(CSRC, s))]
-    files += [os.path.join(ROOT, "include", "cobs.h"), os.path.join(CSRC, BINDING_SRC)]
-    files.append(os.path.abspath(__file__))
-    return max(os.path.getmtime(f) for f in files)
+def binding_path() -> str:
+    """The binding for the running Python and its PyTorch."""
+    import torch
+    return os.path.join(LIB_DIR, f"_paged-{torch.__version__}-{sys.implementation.cache_tag}.so")
+
+
+def _fresh(target: str, sources: list[str]) -> bool:
+    files = [os.path.join(CSRC, s) for s in sources if os.path.exists(os.path.join(CSRC, s))]
+    files += [os.path.join(ROOT, "include", "cobs.h"), os.path.abspath(__file__)]
+    return os.path.exists(target) and os.path.getmtime(target) >= max(os.path.getmtime(f) for f in files)
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -65,7 +69,7 @@ def _build_binding() -> None:
     import sysconfig
 
     from torch.utils import cpp_extension as ext
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = binding_path() + f".tmp{os.getpid()}"
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-w", os.path.join(CSRC, BINDING_SRC), "-o", tmp,
            "-I", sysconfig.get_paths()["include"], "-I", cuda, *[a for d in ext.include_paths() for a in ("-isystem", d)],
@@ -76,12 +80,18 @@ def _build_binding() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"building the paged binding failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, binding_path())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, BINDING)):
-        return LIB
+    if force or not _fresh(LIB, SOURCES + HEADERS):
+        _build_library(verbose)
+    if force or not _fresh(binding_path(), [BINDING_SRC]):
+        _build_binding()
+    return LIB
+
+
+def _build_library(verbose: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
@@ -93,8 +103,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_binding()
-    return LIB
 
 
 if __name__ == "__main__":

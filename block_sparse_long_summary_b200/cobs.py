@@ -14,6 +14,8 @@ import os
 
 import torch
 
+from .build import binding_path
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libcobs.so")
 
@@ -380,7 +382,8 @@ class PagedParams:
         return torch.bfloat16 if self.dtype == "bf16" else torch.float32
 
 
-def _load_binding(path: str = os.path.join(_HERE, "lib", "_paged.so")):
+def _load_binding():
+    path = binding_path()
     if not os.path.exists(path):
         raise ImportError(f"binding of the paged calls not built: {path} is missing "
                           "(run python -m block_sparse_long_summary_b200.build)")

@@ -53,3 +53,20 @@ def test_the_binding_is_loaded_once():
     assert vars(cobs._paged)["attn"] is cobs._paged.attn
     with pytest.raises(AttributeError):
         cobs._paged.no_such_call
+
+
+def test_another_pytorch_gets_a_binding_of_its_own(monkeypatch):
+    import torch
+    B.build()
+    here, made = B.binding_path(), []
+    monkeypatch.setattr(B, "_build_binding", lambda: made.append(B.binding_path()))
+    monkeypatch.setattr(B, "_compile", lambda *a: pytest.fail("the library does not depend on PyTorch"))
+    B.build()
+    assert made == []
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert B.binding_path() != here
+    B.build()
+    assert made == [B.binding_path()]
+    from block_sparse_long_summary_b200 import cobs
+    with pytest.raises(ImportError, match="0.0.1"):
+        cobs._load_binding()
