@@ -92,6 +92,13 @@ struct Call {
     }
 };
 
+// Other Python threads go on while this one is in the library: a launch waits when the device's queue is full,
+// maybe for a function of the host in some stream that itself needs the interpreter.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Runs f, which returns a status; C++ exceptions become Python errors.
 template <typename F>
 PyObject* guarded(Py_ssize_t nargs, Py_ssize_t want, F&& f) {
@@ -121,6 +128,7 @@ PyObject* tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 *kv = c.ints(a[7], "kv_len", c.p.R), *slots = c.ints(a[8], "slot_map", c.p.n_tokens), *counts = c.ints(a[9], "counts", 4);
         const cobs_stream_t s = c.stream(a[10]);
         const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, c.dev));
+        const Unlocked unlocked;
         return cobs_paged_tables(&c.p, cached, fresh, pages, (int32_t)n_free, count, table, cu, kv, slots, counts, s);
     });
 }
@@ -137,6 +145,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void *kc = c.cache(a[4], "k_cache"), *vc = c.cache(a[5], "v_cache");
         const cobs_stream_t s = c.stream(a[6]);
         const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, c.dev));
+        const Unlocked unlocked;
         return cobs_paged_append(&c.p, k, v, slots, kc, vc, s);
     });
 }
@@ -157,6 +166,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* ws = c.flat(a[9], "workspace", at::kByte, bytes);
         const cobs_stream_t s = c.stream(a[10]);
         const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, c.dev));
+        const Unlocked unlocked;
         return cobs_paged_attn(&c.p, q, kc, vc, table, cu, kv, o, lse, ws, (size_t)bytes, s);
     });
 }

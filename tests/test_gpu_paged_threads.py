@@ -75,3 +75,43 @@ def test_float32_chunks_of_different_request_counts():
     for buf, *_ in keep:
         assert (buf.O[0] == 3.0).all() and torch.isfinite(buf.O).all()
     assert C.device_error() == 0
+
+
+STUB = """
+extern int PyGILState_Check(void);
+extern int unlocked(void) { return PyGILState_Check() ? -100 : -200; }
+"""
+CALLS = """
+import importlib.util, sys, torch
+sys.path.insert(0, {root!r})
+from block_sparse_long_summary_b200 import cobs
+spec = importlib.util.spec_from_file_location("_paged", {binding!r})
+paged = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(paged)   # a second copy, which finds the stand-in beside itself
+p = cobs.PagedParams(R=1, Hq=1, Hkv=1, d=64, page=16, n_pages=1, max_pages=1, n_tokens=1, max_new=1)
+buf = cobs.alloc_paged(p)
+i = torch.zeros(1, dtype=torch.int32, device="cuda")
+kv, row = torch.zeros((1, 1, 16, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+print(paged.tables(p.address, i, i, i, i, buf.block_table, buf.cu_new, buf.kv_len, buf.slot_map, buf.counts, None),
+      paged.append(p.address, row, row, buf.slot_map, kv, kv, None),
+      paged.attn(p.address, row, kv, kv, buf.block_table, buf.cu_new, buf.kv_len, buf.O, None, buf.ws, None))
+"""
+
+
+def test_the_library_runs_without_the_interpreter_lock(tmp_path):
+    """The binding beside a stand-in for the library that tells whether its caller holds the lock. (The package's
+    own library is loaded by its path and keeps its symbols to itself.)"""
+    import os
+    import shutil
+    import subprocess
+    import sys
+
+    from block_sparse_long_summary_b200 import build as B
+    cobs()
+    source = STUB + "".join(f"int {f}(void) {{ return unlocked(); }}\n" for f in ("cobs_paged_tables", "cobs_paged_append", "cobs_paged_attn"))
+    (tmp_path / "stub.c").write_text(source)
+    subprocess.run([os.environ.get("CC", "gcc"), "-shared", "-fPIC", "-w", str(tmp_path / "stub.c"), "-o", str(tmp_path / "libcobs.so")], check=True)
+    binding = shutil.copy(B.binding_path(), tmp_path / "_paged.so")
+    r = subprocess.run([sys.executable, "-c", CALLS.format(root=B.ROOT, binding=str(binding))], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split() == ["-200"] * 3, r.stdout
