@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(kTT) paged_tables_kernel(TableArgs a) {
                 c = n = 0;
             }
         }
-        // both sums in one scan: tokens in the low 36 bits (below 2^36: 2^31 per request is cut to
-        // the token rows at once), pages above
+        // tokens before each request, then the pages taken before it, which depend on how many of the tokens have a
+        // row; a request counts at most one token more than there are rows
         n = min(n, a.n_tokens + 1);
         long long all;
         long long inc = block_scan<kTT>(n, tmp[0], all);

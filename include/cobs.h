@@ -342,9 +342,10 @@ cobs_status cobs_block_log_mass(const cobs_params* p, const void* Q, const void*
  * between tokens is q_stride / kv_stride elements, so Q, K and V may be slices of one fused
  * projection. Everything that depends on the lengths is read on the device, so the calls can be
  * captured in a graph and replayed with other lengths.
- * Lengths that contradict each other, the token rows or the table leave a request out (its rows
- * stay as they were); such lengths, and page or slot numbers outside the cache, are recorded in the
- * flag read by cobs_device_error(). */
+ * Lengths that contradict each other, the token rows or the table are recorded in the flag read by
+ * cobs_device_error(), as are page or slot numbers outside the cache. cobs_paged_attn leaves a
+ * request with such lengths out (its rows stay as they were); what cobs_paged_tables makes of them
+ * stands there. */
 typedef struct {
     int32_t R;          /* requests (1 .. 16384): rows of the block table */
     int32_t Hq;         /* query heads */
@@ -374,6 +375,11 @@ typedef struct {
  * order of requests and positions; the caller's next step starts from counts[2] pages. When pages
  * are missing (counts[3] > 0) the entries and slots without a page are -1: the caller drops
  * requests and calls again before it uses them.
+ * A request with a negative length, more than max_new new tokens or more tokens than the table is
+ * wide counts as one of no cached and no new tokens (kv_len 0, no page is taken). When the requests'
+ * new tokens are more than n_tokens, those behind the last token row are cut off: the request that
+ * holds the boundary gets rows, pages and kv_len for its first tokens only, the ones after it for
+ * none. Both are recorded (cobs_device_error()); counts and kv_len tell what was taken.
  * block_table rows, counts and the other outputs must not overlap the inputs. Hq, Hkv, d, window
  * and dtype are not used (but must be valid).
  */
