@@ -363,6 +363,10 @@ class PagedParams:
     def __post_init__(self):
         if self.dtype not in ("bf16", "f32"):
             raise ValueError(f"dtype {self.dtype!r} (bf16 or f32)")
+        for f in dataclasses.fields(self):   # (the struct would keep the low 32 bits)
+            x = getattr(self, f.name)
+            if f.name != "dtype" and not -2 ** 31 <= x < 2 ** 31:
+                raise ValueError(f"{f.name} {x} does not fit 32 bits")
         cp = cobs_paged_params(self.R, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages, self.n_tokens,
                                self.max_new, self.window, self.sinks, COBS_BF16 if self.dtype == "bf16" else COBS_F32, 0, 0)
         object.__setattr__(self, "_struct", cp)

@@ -70,3 +70,17 @@ def test_another_pytorch_gets_a_binding_of_its_own(monkeypatch):
     from block_sparse_long_summary_b200 import cobs
     with pytest.raises(ImportError, match="0.0.1"):
         cobs._load_binding()
+
+
+@pytest.mark.parametrize("name", ["R", "Hq", "Hkv", "d", "page", "n_pages", "max_pages", "n_tokens", "max_new", "window", "sinks"])
+def test_params_that_do_not_fit_the_struct_are_refused(name):
+    import dataclasses
+
+    from block_sparse_long_summary_b200 import cobs
+    p = cobs.PagedParams(R=1, Hq=4, Hkv=1, d=128, page=64, n_pages=4, max_pages=4, n_tokens=1, max_new=1, window=8)
+    for value in (2 ** 31, 2 ** 32 + 1, 2 ** 32, -2 ** 31 - 1, 2 ** 63):
+        with pytest.raises(ValueError, match=name):
+            dataclasses.replace(p, **{name: value})
+    assert getattr(dataclasses.replace(p, **{name: 2 ** 31 - 1}).c(), name) == 2 ** 31 - 1
+    with pytest.raises(TypeError):
+        dataclasses.replace(p, **{name: 1.5})
