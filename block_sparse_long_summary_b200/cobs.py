@@ -423,7 +423,8 @@ def alloc_paged_workspace(p: PagedParams, device="cuda") -> torch.Tensor:
         return torch.empty(n, dtype=torch.uint8, device=dev)
 
 
-# Tensors are checked (device, type, shape, strides) and passed on by the native binding, on `stream` or
+# Tensors are checked (device and type; Q, K and V by shape and strides, the others by their number of elements and
+# for gaps) and passed on by the native binding, on `stream` or
 # the current stream of their device, with that device current.
 
 def cobs_paged_tables(p: PagedParams, cached_len, new_len, free_pages, free_count, block_table, cu_new, kv_len, slot_map,

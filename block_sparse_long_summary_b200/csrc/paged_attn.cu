@@ -11,8 +11,8 @@ namespace {
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 // float32 stays on the CUDA cores. One token per request has at most 16 rows against each key
-// and is a matter of reading the cache: warps with mma.sync take 8 x 32k keys in 168 us where the
-// 128-row tcgen05 tiles take 195 us, one request at 4k keys 10.4 against 15.9 us, 62 ragged ones 67
+// and is a matter of reading the cache: warps with mma.sync take 8 x 32k keys in 171 us where the
+// 128-row tcgen05 tiles take 195 us, one request at 4k keys 10.4 against 15.9 us (on the GPU), 62 ragged ones 69
 // against 95 us. Everything else takes the 128-row tiles.
 enum Kernel { kSimt, kChunk, kDecode };
 Kernel kernel_of(const PagedDims& m) { return m.max_new == 1 ? kDecode : m.dtype == COBS_BF16 ? kChunk : kSimt; }

@@ -1,7 +1,7 @@
 // Native binding of the paged-cache calls: checks the tensors and passes their addresses to the C ABI
 // on the tensors' current stream. A serving step makes these calls a few times per layer while their
-// kernels run for microseconds; through ctypes the checks and the call alone took 5 us of host time, here
-// under 1. Arguments and errors are those of block_sparse_long_summary_b200/cobs.py, which wraps it.
+// kernels run for microseconds: host time per call, launches included, against ctypes on one machine: tables
+// 8.5 -> 4.8 us, append 6.9 -> 4.3 us, attention 11.9 -> 9.5 us (on a faster one 3.5, 3.1 and 5.9 us). Arguments and errors are those of block_sparse_long_summary_b200/cobs.py, which wraps it.
 #include <ATen/core/Tensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDAGuard.h>

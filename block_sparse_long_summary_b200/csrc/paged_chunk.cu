@@ -10,7 +10,10 @@
 //   p = 2^(s c - m)         two threads per row, which exchange their maxima; m moves only when a row's
 //                           maximum grows by more than 2^8 (then the threads rescale their row of
 //                           O, which is seldom)
-//   O_g += P_g V            P in bf16 over S's columns (A operand from TMEM), V MN-major
+//   O_g += P_g V            P in bf16 over S's columns (A operand from TMEM), V MN-major. The MMA takes A and B
+//                           of one type, and a second product with what the rounding leaves would be half as much
+//                           again for the busiest pipe: the error against 64 bits is 2.3e-3, where o's own rounding
+//                           alone gives 1.7e-3 (2048 tokens at 32k keys). The sum of p is not rounded.
 // The two row tiles alternate: while the tensor pipe runs P V of one and the next Q K^T of it, the
 // other one's softmax runs. MMAs are issued by one thread in the order PV_0(k) QK_0(k+1) PV_1(k)
 // QK_1(k+1): the pipe runs them in order, so S_g(k+1) arriving means that P_g(k) has been read and
@@ -26,11 +29,13 @@
 // only the rows that see them change.
 // Every wait is bounded; one that gives up sets the device error flag and the CTA winds down.
 //
-// What bounds it: the chain of a row tile. 2048 tokens at 32k keys, 64 / 4 heads of 128: 1.92 ms, 1112
-// TFLOP/s, 0.67 of the measured bf16 peak; a pair of key tiles takes some 3.9k cycles, of which the tensor pipe
-// has work for 2.1k and the special-function unit for 2.05k. In a trace a row tile's P V and Q K^T take
-// 1.6k cycles with their hand-over, its softmax 2.2k (maxima 0.4k, powers 1.5k), and two row tiles are
-// all that tensor memory holds (two S of 128 columns, two O of d). Measured and left out: key tiles in
+// What bounds it: the chain of a row tile. 2048 tokens at 32k keys, 64 / 4 heads of 128: 2.17-2.20 ms, 970-980
+// TFLOP/s, 0.59 of the measured bf16 peak (1.92 ms and 0.67 on the fastest machine seen); a key tile of both row
+// tiles takes some 3.9k cycles, of which the tensor pipe has work for 2.1k and the special-function unit for
+// 2.05k. In a trace a row tile's P V and Q K^T take 1.6k cycles with their hand-over, its softmax 2.2k (maxima
+// 0.4k, powers 1.5k), and two row tiles are all that tensor memory holds (two S of 128 columns, two O of d). The
+// softmax reads its scores twice, in masked tiles three times: 96 registers a thread do not hold them beside the
+// rest. Measured and left out: key tiles in
 // halves with N = 64 (four streams, but Q K^T is then bound by shared memory: half as fast); powers partly
 // on the FMA pipes (7% slower and more); P handed over in halves (3%); scores kept in registers between
 // maxima and powers (spills), or read 16 at a time (18%).

@@ -6,8 +6,8 @@
 //
 // One CTA per SM walks its range of (unit, 128-key tile) pairs (paged_plan.cuh); a unit is one request
 // and KV head, its rows the G heads of the group. Warp w takes keys 16 w .. + 15 of every tile, by
-// itself: it copies them (cp.async, 16 bytes a lane, into the 128-byte swizzle) two or three tiles
-// ahead, over the ends of units, and needs no barrier until the unit's end, where the eight warps'
+// itself: it copies them (cp.async, 16 bytes a lane, into the 128-byte swizzle) two tiles ahead (one for
+// more than 8 heads a group), over the ends of units, and needs no barrier until the unit's end, where the eight warps'
 // maxima, sums and outputs are joined through shared memory. Rows that the token does not see are
 // filled with zeros by the copy, so nothing they hold gets in.
 // A warp's step is transposed: S^T = K Q^T with the keys as the 16 rows of mma.sync m16n8k16 and the

@@ -7,11 +7,13 @@
 //
 // One CTA per SM walks its range of (unit, 64-key tile) pairs (paged_plan.cuh); a unit is one request and KV
 // head, its rows the G heads of the group. Warp w takes keys 8 w .. + 7 of every tile, by itself: it copies
-// them (cp.async) two or three tiles ahead, over the ends of units, and needs no barrier until the unit's
+// them (cp.async) two tiles ahead (one for more than 8 heads), over the ends of units, and needs no barrier until the unit's
 // end, where the eight warps' maxima, sums and outputs are joined through shared memory. Rows that the
 // token does not see are filled with zeros by the copy. For the scores lane 4 r + q takes key r of the
 // slice and every fourth 16 bytes of its row, for P V every lane takes d / 32 columns.
-// 4 x 2000 keys of 8 heads: 29 us per call, against 55 us as a 16-row case of the chunk kernel.
+// 4 x 2000 keys of 8 heads, groups of 4: 29 us per call, against 55 us as a 16-row case of the chunk kernel; 8 x 32768
+// keys 467 us, 0.70 of the copy bandwidth. With groups of 16 the products bound it (2 heads of 8 x 32768 keys: 325 us,
+// 0.25): the heads come one after another, and each reads the slice's V from shared memory and Q through L1 again.
 #include <algorithm>
 
 #include "paged.h"

@@ -44,7 +44,15 @@ struct PagedArgs {
     int rec_rows;
     int* err;
     int R, Hq, Hkv, G, page, page_shift, n_pages, max_pages, n_tokens, max_new, W, S;
-    int lead_one, lead_two; // a unit's start and end in tiles, for one and two row tiles (measured at 1 to 6)
+    // a unit's start and end in tiles, for one and two row tiles. us per call at (one, two):
+    //   bf16 chunks     (1, 1)  (1, 2)  (2, 2)  (2, 3)  (3, 4)  (4, 6)
+    //   mixed            238.0   229.4   229.8   231.4   234.6   239.9
+    //   with a window    162.9   160.1   160.1   157.7   156.9   155.1     (a long chunk: 2.20 ms at each)
+    //   single tokens        1       2       3       4       6
+    //   62 ragged         74.9    69.0    70.8    74.1    79.4             (8 x 32k keys: 171-173 at each)
+    //   with a window     24.6    23.0    23.5    24.4    24.7
+    //   float32 chunks   147.8   151.5   150.1
+    int lead_one, lead_two;
     float sl2;              // log2(e) / sqrt(d)
 };
 

@@ -236,7 +236,7 @@ cudaError_t run(const PagedArgs& a, int workers, const float* Q, long long q_str
 
 }  // namespace
 
-// 16 rows where no request has more (a single token's heads): a tile's products are then a quarter.
+// 16 rows where no request has more (a few tokens of few heads): a tile's products are then a quarter.
 static int simt_rows(const PagedDims& m) { return (long long)m.max_new * m.G <= 16 ? 16 : 64; }
 
 int paged_simt_rec_rows(const PagedDims& m) { return simt_rows(m); }
