@@ -402,8 +402,10 @@ class _Binding:
     of PyTorch, which the other calls do not depend on."""
 
     def __getattr__(self, name):
-        vars(self).update((f, getattr(module, f)) for module in [_load_binding()] for f in ("tables", "append", "attn"))
-        return object.__getattribute__(self, name)
+        if name not in ("tables", "append", "attn"):   # (what looks the object over loads nothing)
+            raise AttributeError(name)
+        vars(self)[name] = f = getattr(_load_binding(), name)
+        return f
 
 
 _paged = _Binding()

@@ -27,6 +27,7 @@ from block_sparse_long_summary_b200 import cobs
 assert cobs.version() > 0 and cobs.workspace_bytes(cobs.Params(B=1, Hq=4, Hkv=1, d=128, T=4096, topk=8, window=512), cobs.COBS_WS_DECODE) > 0
 p = cobs.PagedParams(R=1, Hq=4, Hkv=1, d=128, page=64, n_pages=4, max_pages=4, n_tokens=1, max_new=1)
 assert cobs.paged_workspace_bytes(p) > 0
+assert not hasattr(cobs._paged, "__wrapped__")   # looking the package over does not load the binding
 for _ in range(2):
     try:
         cobs.cobs_paged_append(p, None, None, None, None, None)
@@ -50,7 +51,7 @@ def test_the_binding_is_loaded_once():
     with pytest.raises(TypeError, match="tensor"):
         cobs.cobs_paged_append(cobs.PagedParams(R=1, Hq=4, Hkv=1, d=128, page=64, n_pages=4, max_pages=4, n_tokens=1, max_new=1),
                                None, None, None, None, None)
-    assert vars(cobs._paged)["attn"] is cobs._paged.attn
+    assert vars(cobs._paged)["append"] is cobs._paged.append
     with pytest.raises(AttributeError):
         cobs._paged.no_such_call
 
